@@ -94,6 +94,22 @@ def lib() -> ctypes.CDLL:
         L.bitnet_ste_weight_workspace_bytes.restype = ctypes.c_size_t
         L.bitnet_ste_backward_weight.argtypes = [P, P, P, I64, I64, I64, P, I, P, ctypes.c_size_t, P]
         L.bitnet_ste_backward_weight.restype = I
+        L.bitnet_act_checkpoint.argtypes = [P, I, I64, I64, P, P, P]
+        L.bitnet_act_checkpoint.restype = I
+        L.bitnet_act_restore.argtypes = [P, P, I64, I64, P, I, P]
+        L.bitnet_act_restore.restype = I
+        L.bitnet_layernorm.argtypes = [P, I, I64, I64, P, P, F, P, P, P, P, P, P]
+        L.bitnet_layernorm.restype = I
+        L.bitnet_norm_backward_workspace_bytes.argtypes = [I64, I64]
+        L.bitnet_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.bitnet_layernorm_backward.argtypes = [P, I, I64, I64, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.bitnet_layernorm_backward.restype = I
+        L.bitnet_rmsnorm_backward.argtypes = [P, I, I64, I64, P, P, P, P, F, P, P, P, ctypes.c_size_t, P]
+        L.bitnet_rmsnorm_backward.restype = I
+        L.bitnet_relu2_gate.argtypes = [P, P, I, I64, I64, P, P, P, P, P, P]
+        L.bitnet_relu2_gate.restype = I
+        L.bitnet_relu2_gate_backward.argtypes = [P, I, I64, I64, P, P, P, P, P, P, P, P, P]
+        L.bitnet_relu2_gate_backward.restype = I
         L.bitnet_get_device_status.argtypes = [P]
         L.bitnet_get_device_status.restype = I
         L.bitnet_status_string.argtypes = [I]
@@ -520,6 +536,211 @@ def bitnet_ste_backward_weight(dY, x_q, a_scale, dW=None, out_dtype=None, worksp
                                           workspace.numel() * workspace.element_size(), _stream(dY.device))
     _check("bitnet_ste_backward_weight", st)
     return dW
+
+
+# ------------------------------------------------- between the products of a training step
+
+ACT8_GROUP = 64  # columns of a row that share a scale in an 8-bit copy
+
+
+def _launch(name: str, device, *args) -> None:
+    """Calls an entry point on the current stream of `device`, with that device current."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        st = getattr(lib(), name)(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), name)(*args, _stream(device))
+    if st != BITNET_OK:
+        raise BitnetError(name, st)
+
+
+def _matrix(name: str, t):
+    """Rows, columns, dtype, dtype code and device of a contiguous M x K float tensor on a CUDA device."""
+    _need_cuda(t)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    code = _dtype_code(t.dtype)
+    if code == BITNET_I32:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return t.shape[0], t.shape[1], t.dtype, code, t.device
+
+
+def _expect(name: str, t, shape, dtype, device):
+    """Refuses a tensor that does not have this shape, type and device; None passes."""
+    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _output(name: str, t, shape, dtype, device):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    return _expect(name, t, shape, dtype, device)
+
+
+def _copy_of(name: str, x8, x_scale, M: int, K: int, device) -> None:
+    """Checks an 8-bit copy of an M x K activation that a call reads."""
+    torch = _torch()
+    if x8 is None or x_scale is None:
+        raise ValueError(f"the 8-bit copy of {name} needs its codes and its scales")
+    _expect(f"{name}8", x8, (M, K), torch.int8, device)
+    _expect(f"{name}_scale", x_scale, (M, K // ACT8_GROUP), torch.float32, device)
+
+
+def bitnet_act_checkpoint(x, x8=None, x_scale=None):
+    """x (M x K float32 or bfloat16) in 8 bits for the backward pass: int8 codes
+    and one float32 scale per row and 64 columns.  Returns (x8, x_scale)."""
+    torch = _torch()
+    M, K, _, code, dev = _matrix("x", x)
+    x8 = _output("x8", x8, (M, K), torch.int8, dev)
+    x_scale = _output("x_scale", x_scale, (M, K // ACT8_GROUP), torch.float32, dev)
+    _launch("bitnet_act_checkpoint", dev, _ptr(x), code, M, K, _ptr(x8), _ptr(x_scale))
+    return x8, x_scale
+
+
+def bitnet_act_restore(x8, x_scale, out_dtype=None, x=None):
+    """The values of an 8-bit copy as an M x K tensor of out_dtype (bfloat16 by default)."""
+    torch = _torch()
+    _need_cuda(x8)
+    if x8.dim() != 2:
+        raise ValueError("x8 must be a matrix")
+    (M, K), dev = x8.shape, x8.device
+    _copy_of("x", x8, x_scale, M, K, dev)
+    x = _output("x", x, (M, K), out_dtype or (torch.bfloat16 if x is None else x.dtype), dev)
+    _launch("bitnet_act_restore", dev, _ptr(x8), _ptr(x_scale), M, K, _ptr(x), _dtype_code(x.dtype))
+    return x
+
+
+def bitnet_layernorm(x, gain=None, bias=None, eps: float = 1e-5, checkpoint: bool = False, y=None, mean=None,
+                     rstd=None, x8=None, x_scale=None):
+    """Layer norm of the rows of x (M x K float32 or bfloat16); gain and bias: K
+    values of x's type, or None.  Returns (y, mean, rstd), and with checkpoint
+    also x's 8-bit copy, written in the same pass: (y, mean, rstd, x8, x_scale)."""
+    torch = _torch()
+    M, K, dt, code, dev = _matrix("x", x)
+    _expect("gain", gain, (K,), dt, dev)
+    _expect("bias", bias, (K,), dt, dev)
+    y = _output("y", y, (M, K), dt, dev)
+    mean = _output("mean", mean, (M,), torch.float32, dev)
+    rstd = _output("rstd", rstd, (M,), torch.float32, dev)
+    if checkpoint:
+        x8 = _output("x8", x8, (M, K), torch.int8, dev)
+        x_scale = _output("x_scale", x_scale, (M, K // ACT8_GROUP), torch.float32, dev)
+    elif x8 is not None or x_scale is not None:
+        raise ValueError("x8 and x_scale are outputs of checkpoint=True")
+    _launch("bitnet_layernorm", dev, _ptr(x), code, M, K, _ptr(gain), _ptr(bias), eps, _ptr(y), _ptr(mean),
+            _ptr(rstd), _ptr(x8), _ptr(x_scale))
+    return (y, mean, rstd, x8, x_scale) if checkpoint else (y, mean, rstd)
+
+
+def bitnet_norm_backward_workspace_bytes(M: int, K: int) -> int:
+    """Workspace bytes of the norms' backward passes on the current device."""
+    return int(lib().bitnet_norm_backward_workspace_bytes(M, K))
+
+
+def _norm_backward_args(dy, x, x8, x_scale, gain, dx, want, workspace):
+    """The checks and buffers that both norms' backward passes share."""
+    torch = _torch()
+    M, K, dt, code, dev = _matrix("dy", dy)
+    if (x is None) == (x8 is None):
+        raise ValueError("give x, or its 8-bit copy as x8 and x_scale")
+    if x is None:
+        _copy_of("x", x8, x_scale, M, K, dev)
+    else:
+        if x_scale is not None:
+            raise ValueError("x_scale belongs to x8")
+        _expect("x", x, (M, K), dt, dev)
+    _expect("gain", gain, (K,), dt, dev)
+    dx = _output("dx", dx, (M, K), dt, dev)
+    if want and workspace is None:
+        with torch.cuda.device(dev):
+            nbytes = bitnet_norm_backward_workspace_bytes(M, K)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif workspace is not None:
+        _need_cuda(workspace)
+        if workspace.device != dev:
+            raise ValueError(f"workspace must live on {dev}")
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return M, K, code, dev, dx, workspace, wsb
+
+
+def bitnet_layernorm_backward(dy, mean, rstd, x=None, x8=None, x_scale=None, gain=None, dx=None, dgain=None,
+                              dbias=None, want_dgain: bool = True, want_dbias: bool = True, workspace=None):
+    """Gradients of layer norm from dy (M x K) and x, or x's 8-bit copy; mean and
+    rstd as bitnet_layernorm returned them.  Returns (dx, dgain, dbias): dx of
+    dy's type, dgain and dbias float32 [K], or None where not wanted.
+    workspace: a uint8 device tensor of bitnet_norm_backward_workspace_bytes
+    bytes, reused across calls on one stream (allocated for this call when None)."""
+    torch = _torch()
+    M, K, code, dev, dx, workspace, wsb = _norm_backward_args(dy, x, x8, x_scale, gain, dx,
+                                                              want_dgain or want_dbias, workspace)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward pass are needed")
+    _expect("mean", mean, (M,), torch.float32, dev)
+    _expect("rstd", rstd, (M,), torch.float32, dev)
+    dgain = _output("dgain", dgain, (K,), torch.float32, dev) if want_dgain else None
+    dbias = _output("dbias", dbias, (K,), torch.float32, dev) if want_dbias else None
+    _launch("bitnet_layernorm_backward", dev, _ptr(dy), code, M, K, _ptr(x), _ptr(x8), _ptr(x_scale), _ptr(mean),
+            _ptr(rstd), _ptr(gain), _ptr(dx), _ptr(dgain), _ptr(dbias), _ptr(workspace), wsb)
+    return dx, dgain, dbias
+
+
+def bitnet_rmsnorm_backward(dy, x=None, x8=None, x_scale=None, gain=None, rms_eps: float = 1e-5, dx=None, dgain=None,
+                            want_dgain: bool = True, workspace=None):
+    """Gradients of the RMSNorm in front of a BitLinear from dy (M x K, the
+    gradient of the normalised input) and x, or x's 8-bit copy.  Returns
+    (dx, dgain): dx of dy's type, dgain float32 [K] or None where not wanted.
+    workspace: as in bitnet_layernorm_backward."""
+    torch = _torch()
+    M, K, code, dev, dx, workspace, wsb = _norm_backward_args(dy, x, x8, x_scale, gain, dx, want_dgain, workspace)
+    dgain = _output("dgain", dgain, (K,), torch.float32, dev) if want_dgain else None
+    _launch("bitnet_rmsnorm_backward", dev, _ptr(dy), code, M, K, _ptr(x), _ptr(x8), _ptr(x_scale), _ptr(gain),
+            rms_eps, _ptr(dx), _ptr(dgain), _ptr(workspace), wsb)
+    return dx, dgain
+
+
+def bitnet_relu2_gate(u, g, checkpoint: bool = False, h=None, u8=None, u_scale=None, g8=None, g_scale=None):
+    """h = relu(g)^2 * u (M x F, the type of u and g).  Returns h, and with
+    checkpoint also the 8-bit copies of u and g, written in the same pass:
+    (h, u8, u_scale, g8, g_scale)."""
+    torch = _torch()
+    M, F, dt, code, dev = _matrix("u", u)
+    _expect("g", g, (M, F), dt, dev)
+    h = _output("h", h, (M, F), dt, dev)
+    if checkpoint:
+        u8 = _output("u8", u8, (M, F), torch.int8, dev)
+        g8 = _output("g8", g8, (M, F), torch.int8, dev)
+        u_scale = _output("u_scale", u_scale, (M, F // ACT8_GROUP), torch.float32, dev)
+        g_scale = _output("g_scale", g_scale, (M, F // ACT8_GROUP), torch.float32, dev)
+    elif not (u8 is None and u_scale is None and g8 is None and g_scale is None):
+        raise ValueError("u8, u_scale, g8 and g_scale are outputs of checkpoint=True")
+    _launch("bitnet_relu2_gate", dev, _ptr(u), _ptr(g), code, M, F, _ptr(h), _ptr(u8), _ptr(u_scale), _ptr(g8),
+            _ptr(g_scale))
+    return (h, u8, u_scale, g8, g_scale) if checkpoint else h
+
+
+def bitnet_relu2_gate_backward(dh, u=None, g=None, u8=None, u_scale=None, g8=None, g_scale=None, du=None, dg=None):
+    """Gradients of the squared-ReLU gate from dh (M x F) and u and g, or their
+    8-bit copies.  Returns (du, dg), of dh's type."""
+    M, F, dt, code, dev = _matrix("dh", dh)
+    if u8 is None and g8 is None:
+        if u is None or g is None or u_scale is not None or g_scale is not None:
+            raise ValueError("give u and g, or their 8-bit copies")
+        _expect("u", u, (M, F), dt, dev)
+        _expect("g", g, (M, F), dt, dev)
+    else:
+        if u is not None or g is not None:
+            raise ValueError("give u and g, or their 8-bit copies")
+        _copy_of("u", u8, u_scale, M, F, dev)
+        _copy_of("g", g8, g_scale, M, F, dev)
+    du = _output("du", du, (M, F), dt, dev)
+    dg = _output("dg", dg, (M, F), dt, dev)
+    _launch("bitnet_relu2_gate_backward", dev, _ptr(dh), code, M, F, _ptr(u), _ptr(g), _ptr(u8), _ptr(u_scale),
+            _ptr(g8), _ptr(g_scale), _ptr(du), _ptr(dg))
+    return du, dg
 
 
 def bitnet_get_device_status(device=None) -> int:

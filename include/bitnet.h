@@ -492,6 +492,106 @@ bitnet_status bitnet_bitlinear_ffn_gemv(const void* x, int x_dtype, int64_t M, i
                                         void* stream);
 
 /*
+ * Between the products of a training step: the norms and the squared-ReLU
+ * gate with their gradients, and the activations that the backward pass reads
+ * kept in 8 bits.  All activations, gradients of activations, gains and
+ * biases of one call have the type `dtype` (BITNET_F32 or BITNET_BF16);
+ * statistics, scales and the gradients of gain and bias are fp32.  Sums are
+ * fp32 in a fixed order, so a call repeated on the same device gives the same
+ * bits; results are rounded once, when they are stored.  Outputs must not
+ * overlap inputs or each other.  Scales and statistics need 4-byte alignment
+ * only.  Asynchronous; nothing of a call survives it but its outputs.
+ *
+ * The 8-bit copy of an M x K activation x: per row and group of 64 columns
+ *
+ *   amax = max |x|,  scale = RN32(amax / 127)
+ *   x8   = RNE(RN32(x * RN32(127 / amax)))             in [-127, 127]
+ *
+ * the rule of bitnet_quant_act with a group in the place of a row.  A group
+ * whose amax is below 2^-120 gets scale 0 and codes 0; a group that holds an
+ * Inf or a NaN gets scale NaN and codes 0, so that all of it restores to NaN.
+ * The scale is at most FLT_MAX / 127 rounded down, so that finite values
+ * restore to finite ones.
+ * x8 is M x K int8, x_scale is M x K/64 fp32, row-major.  The restored value is
+ * RN32(x8 * x_scale): within scale / 2 of x, up to the three fp32 roundings.
+ *
+ * bitnet_act_checkpoint: x (M x K of x_dtype) -> x8, x_scale.
+ * bitnet_act_restore:    x8, x_scale -> x (M x K of x_dtype).
+ * 1 <= M <= INT32_MAX, M * K <= 2^40.
+ */
+bitnet_status bitnet_act_checkpoint(const void* x, int x_dtype, int64_t M, int64_t K, int8_t* x8, float* x_scale,
+                                    void* stream);
+bitnet_status bitnet_act_restore(const int8_t* x8, const float* x_scale, int64_t M, int64_t K, void* x, int x_dtype,
+                                 void* stream);
+
+/*
+ * Layer norm of M rows of K values, 1 <= M <= INT32_MAX, K <= 32768:
+ *
+ *   mean = sum x / K,  rstd = 1 / sqrt(sum (x - mean)^2 / K + eps)
+ *   y    = (x - mean) * rstd * gain + bias
+ *
+ * gain, bias    [in]  K values of `dtype`, or NULL for 1 and 0.
+ * eps           [in]  finite, > 0.
+ * mean, rstd    [out] M fp32 each for the backward pass, or NULL.
+ * x8, x_scale   [out] the 8-bit copy of x, written in the same pass, or both
+ *                     NULL.
+ */
+bitnet_status bitnet_layernorm(const void* x, int dtype, int64_t M, int64_t K, const void* gain, const void* bias,
+                               float eps, void* y, float* mean, float* rstd, int8_t* x8, float* x_scale,
+                               void* stream);
+
+/*
+ * Gradients of layer norm, and of the RMSNorm that bitnet_quant_act and the
+ * fused BitLinear calls apply (h = x * r * gain, r = 1 / sqrt(sum x^2 / K +
+ * rms_eps)).  With t = dy * gain and n = (x - mean) * rstd, or n = x * r:
+ *
+ *   dx    = rstd * (t - sum t / K - n * sum(t * n) / K)       layer norm
+ *   dx    = r * (t - n * sum(t * n) / K)                      RMSNorm
+ *   dgain = sum over rows of dy * n,  dbias = sum over rows of dy
+ *
+ * dy          [in]  M x K of `dtype`: the gradient of the norm's output.
+ * x           [in]  M x K of `dtype`, or NULL with
+ * x8, x_scale [in]  its 8-bit copy (exactly one of the two forms is given).
+ *                   Layer norm takes the statistics of the exact x from
+ *                   mean and rstd; RMSNorm computes r from the values read.
+ * mean, rstd  [in]  M fp32 each, as bitnet_layernorm left them.
+ * gain        [in]  K of `dtype`, or NULL for 1.
+ * dx          [out] M x K of `dtype`.
+ * dgain, dbias [out] K fp32 each, 16-byte aligned; either may be NULL.
+ * workspace   [in]  bitnet_norm_backward_workspace_bytes(M, K) bytes on the
+ *                   current device; contents do not matter before or after.
+ *                   Calls that can run at the same time must not share it.
+ *                   NULL where dgain and dbias are NULL.
+ */
+size_t bitnet_norm_backward_workspace_bytes(int64_t M, int64_t K);
+bitnet_status bitnet_layernorm_backward(const void* dy, int dtype, int64_t M, int64_t K, const void* x,
+                                        const int8_t* x8, const float* x_scale, const float* mean, const float* rstd,
+                                        const void* gain, void* dx, float* dgain, float* dbias, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+bitnet_status bitnet_rmsnorm_backward(const void* dy, int dtype, int64_t M, int64_t K, const void* x, const int8_t* x8,
+                                      const float* x_scale, const void* gain, float rms_eps, void* dx, float* dgain,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The FFN's squared-ReLU gate on its own, for a training step that keeps u and
+ * g (bitnet_linear_upgate_gemm keeps neither), and its gradient:
+ *
+ *   h  = RN32(RN32(r * r) * u) rounded to `dtype`,  r = g if g > 0, else +0
+ *   du = dh * r^2,  dg = dh * u * 2r
+ *
+ * u, g, h, dh, du, dg: M x F of `dtype`, M and F as M and K above.
+ * bitnet_relu2_gate writes the 8-bit copies of u and g in the same pass when
+ * u8, u_scale, g8 and g_scale are given (all four or none).
+ * bitnet_relu2_gate_backward reads u and g, or the copies (all of one form,
+ * none of the other).
+ */
+bitnet_status bitnet_relu2_gate(const void* u, const void* g, int dtype, int64_t M, int64_t F, void* h, int8_t* u8,
+                                float* u_scale, int8_t* g8, float* g_scale, void* stream);
+bitnet_status bitnet_relu2_gate_backward(const void* dh, int dtype, int64_t M, int64_t F, const void* u, const void* g,
+                                         const int8_t* u8, const float* u_scale, const int8_t* g8,
+                                         const float* g_scale, void* du, void* dg, void* stream);
+
+/*
  * Synchronises `stream`, then reports and clears the device-side error word
  * that kernels set when a bounded wait on a barrier runs out (they then skip
  * their remaining work and exit instead of hanging).  Returns BITNET_OK,
