@@ -2,6 +2,7 @@
 // RMSNorm (norm.cuh).
 #include "host_common.h"
 #include "norm.cuh"
+#include "norm_bwd.cuh"
 
 #include <algorithm>
 
@@ -11,6 +12,22 @@ using namespace bitnet;
 using namespace bitnet_host;
 
 constexpr int64_t kNormMaxK = 32768;
+
+// How a backward pass deals out its columns (measured, us a call in a graph):
+// 8 columns per thread up to K = 1024 (M = 4096, K = 640: 9.3 against 10.9 with
+// 16, M = 333 f32: 4.8 against 5.8), 16 beyond; a CTA per row up to K = 4096
+// and a cluster of CTAs of at most 256 threads beyond (M = 2048, K = 5376: 19.6
+// against 20.2 in one CTA; M = 4096, K = 6912: 36.9 against 40.5).
+constexpr int64_t kNormNarrowK = 1024;
+constexpr int64_t kNormOneCtaK = 4096;
+constexpr int kNormClusterThreads = 256;
+// CTAs per SM, at most.  A CTA without a cluster holds several teams up to 512
+// threads, so one per SM is enough, and leaves fewer partial rows to join
+// (M = 4096, K = 2560: 21.1 us with three CTAs per SM, 18.9 with three teams).
+constexpr int kNormCtasPerSm = 1;
+constexpr int kNormClusterCtasPerSm = 4;
+constexpr int kSmemPerSm = 233472;  // 228 KB
+constexpr int kNormBwdSmemMax = 220 * 1024;
 
 bool valid_rows(int64_t M, int64_t K) { return valid_k(K) && K <= kNormMaxK && M >= 1 && M <= INT32_MAX; }
 
@@ -25,23 +42,120 @@ cudaError_t launch_layernorm(const void* x, int64_t M, int K, const void* gain, 
                     x_scale);
 }
 
-// Partial sums of the columns: rows are dealt to this many CTAs per column strip.
-int column_parts(int64_t M, int K) {
-  const int strips = (K + 255) / 256;
-  const int64_t want = std::max<int64_t>(1, 8 * static_cast<int64_t>(sm_count()) / strips);
-  return static_cast<int>(std::min<int64_t>(want, (M + 7) / 8));
+// How the columns of a backward pass are dealt out: independent of the types,
+// as the workspace follows from it.
+struct NormPlan {
+  int cv;     // columns per thread
+  int split;  // CTAs (a cluster) per row
+  int cols;   // columns per CTA
+  int team;   // threads per row and CTA
+};
+
+NormPlan norm_plan(int64_t K) {
+  NormPlan p;
+  p.cv = K <= kNormNarrowK ? 8 : 16;
+  const int64_t want = (K + p.cv - 1) / p.cv;
+  p.split = K <= kNormOneCtaK ? 1 : static_cast<int>((want + kNormClusterThreads - 1) / kNormClusterThreads);
+  p.cols = static_cast<int>((K / 64 + p.split - 1) / p.split) * 64;
+  p.split = static_cast<int>((K + p.cols - 1) / p.cols);
+  p.team = (((p.cols + p.cv - 1) / p.cv) + 31) / 32 * 32;
+  return p;
+}
+
+// Clusters (CTAs when split is 1) that a pass uses at most.
+int64_t norm_most_parts(const NormPlan& p, int64_t M) {
+  const int64_t ctas = static_cast<int64_t>(sm_count()) * (p.split > 1 ? kNormClusterCtasPerSm : kNormCtasPerSm);
+  return std::min<int64_t>(M, ctas / p.split);
+}
+
+template <typename F>
+int kernel_registers(F* fn, std::atomic<int> (&cache)[kMaxDevices]) {
+  const int d = current_device();
+  int n = d >= 0 && d < kMaxDevices ? cache[d].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaFuncAttributes fa;
+    n = cudaFuncGetAttributes(&fa, fn) == cudaSuccess ? fa.numRegs : 128;
+    if (d >= 0 && d < kMaxDevices) cache[d].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Clusters of this launch that run at the same time (GPCs hold a whole number
+// of them, so it can be less than the SMs would suggest); the last answer is
+// kept per kernel and device as (key << 16 | answer).
+template <typename F>
+int64_t active_clusters(F* fn, const cudaLaunchConfig_t& cfg, int split, std::atomic<uint64_t> (&cache)[kMaxDevices]) {
+  const int d = current_device();
+  const uint64_t key = (static_cast<uint64_t>(cfg.dynamicSmemBytes) << 16 | cfg.blockDim.x) << 4 | static_cast<uint64_t>(split);
+  if (d >= 0 && d < kMaxDevices) {
+    const uint64_t c = cache[d].load(std::memory_order_relaxed);
+    if (c >> 16 == key) return static_cast<int64_t>(c & 0xFFFF);
+  }
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) n = 1;
+  if (d >= 0 && d < kMaxDevices) cache[d].store(key << 16 | static_cast<uint64_t>(n), std::memory_order_relaxed);
+  return n;
+}
+
+template <typename T, bool COPY, bool RMS, int MODE, int C, int R>
+cudaError_t launch_norm_bwd(const NormBwd& a, const NormPlan& p, cudaStream_t s) {
+  static std::atomic<bool> done[kMaxDevices] = {};
+  static std::atomic<int> regs[kMaxDevices] = {};
+  auto kern = norm_bwd_kernel<T, COPY, RMS, MODE, C, R>;
+  int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(kNormMaxTeams, kNormBwdThreads / p.team));
+  while (teams > 1 && norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols) > kNormBwdSmemMax) --teams;
+  const int threads = teams * p.team;
+  const int smem = norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols);
+  cudaError_t e = set_smem(kern, kNormBwdSmemMax, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.split));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int64_t parts = std::min(norm_most_parts(p, a.M), (a.M + teams - 1) / teams);
+  if constexpr (MODE == kClusterTeam) {
+    static std::atomic<uint64_t> clusters[kMaxDevices] = {};
+    if (parts > sm_count() / 2 / p.split) parts = std::min(parts, active_clusters(kern, cfg, p.split, clusters));
+    cfg.numAttrs = 2;
+  } else {
+    const int by_regs = 65536 / ((kernel_registers(kern, regs) + 7) / 8 * 8 * threads);
+    const int by_smem = kSmemPerSm / (smem + 4096);
+    parts = std::min(parts, static_cast<int64_t>(sm_count()) * std::max(1, std::min(by_regs, by_smem)));
+    cfg.attrs = attr + 1;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(parts * p.split));
+  e = cudaLaunchKernelEx(&cfg, kern, a, p.team, p.split, p.cols);
+  if (e != cudaSuccess || parts == 1 || (a.dgain == nullptr && a.dbias == nullptr)) return e;
+  return launch_pdl(norm_join_kernel, dim3(static_cast<unsigned>(a.K / (4 * kNormJoinLanes)), a.dbias != nullptr ? 2 : 1),
+                    dim3(kNormJoinThreads), 0, s, static_cast<const float*>(a.part), static_cast<int>(parts), a.K,
+                    a.dgain, a.dbias);
 }
 
 template <typename T, bool COPY, bool RMS>
 cudaError_t launch_norm_backward_t(const NormBwd& a, cudaStream_t s) {
-  cudaError_t e = launch_pdl(norm_dx_kernel<T, COPY, RMS>, dim3(static_cast<unsigned>(a.M)), dim3(kNormThreads), 0, s, a);
-  if (e != cudaSuccess || (a.dgain == nullptr && a.dbias == nullptr)) return e;
-  const int P = column_parts(a.M, a.K);
-  const unsigned strips = static_cast<unsigned>((a.K + 255) / 256);
-  e = launch_pdl(norm_columns_kernel<T, COPY, RMS>, dim3(strips, P), dim3(kNormThreads), 0, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(norm_columns_join_kernel, dim3(strips, 2), dim3(kNormThreads), 0, s,
-                    static_cast<const float*>(a.part), P, a.K, a.dgain, a.dbias);
+  constexpr int V = Piece<T>::V;
+  static_assert(kNormNarrowK <= kNormOneCtaK && kNormNarrowK <= 8 * kNormBwdThreads &&
+                    kNormOneCtaK <= 16 * kNormBwdThreads,
+                "a CTA takes a whole row");
+  static_assert(kNormMaxK <= 8 * 16 * kNormClusterThreads && kNormClusterThreads / 32 * 8 <= kNormMaxWarpSums,
+                "a portable cluster takes the longest row");
+  // four rows a batch where they are small (8-bit copies in clusters: M = 4096,
+  // K = 6912 36.2 us against 39.2 with two)
+  const NormPlan p = norm_plan(a.K);
+  if (p.split > 1) return launch_norm_bwd<T, COPY, RMS, kClusterTeam, 16 / V, COPY && sizeof(T) == 2 ? 4 : 2>(a, p, s);
+  if (p.cv == 16) return launch_norm_bwd<T, COPY, RMS, kCtaTeam, 16 / V, 2>(a, p, s);
+  if (p.team == 32) return launch_norm_bwd<T, COPY, RMS, kWarpTeam, 8 / V, 4>(a, p, s);
+  return launch_norm_bwd<T, COPY, RMS, kCtaTeam, 8 / V, 4>(a, p, s);
 }
 
 template <bool RMS>
@@ -91,8 +205,7 @@ bitnet_status bitnet_layernorm(const void* x, int dtype, int64_t M, int64_t K, c
 
 size_t bitnet_norm_backward_workspace_bytes(int64_t M, int64_t K) {
   if (!valid_rows(M, K)) return 0;
-  const size_t parts = static_cast<size_t>(column_parts(M, static_cast<int>(K)));
-  return 2 * parts * static_cast<size_t>(K) * sizeof(float) + static_cast<size_t>(M) * sizeof(float);
+  return 2 * static_cast<size_t>(norm_most_parts(norm_plan(K), M)) * static_cast<size_t>(K) * sizeof(float);
 }
 
 bitnet_status bitnet_layernorm_backward(const void* dy, int dtype, int64_t M, int64_t K, const void* x,
@@ -104,7 +217,7 @@ bitnet_status bitnet_layernorm_backward(const void* dy, int dtype, int64_t M, in
       check_norm_backward(dy, dtype, M, K, x, x8, x_scale, gain, dx, dgain, dbias, workspace, workspace_bytes);
   if (st != BITNET_OK) return st;
   const NormBwd a = {dy,    x,  x8,    x_scale, mean,  rstd, gain,
-                     dx,    dgain, dbias, static_cast<float*>(workspace), nullptr, 0.0f, M, static_cast<int>(K)};
+                     dx,    dgain, dbias, static_cast<float*>(workspace), 0.0f, M, static_cast<int>(K)};
   return from_cuda(launch_norm_backward<false>(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -115,10 +228,8 @@ bitnet_status bitnet_rmsnorm_backward(const void* dy, int dtype, int64_t M, int6
   const bitnet_status st =
       check_norm_backward(dy, dtype, M, K, x, x8, x_scale, gain, dx, dgain, nullptr, workspace, workspace_bytes);
   if (st != BITNET_OK) return st;
-  float* part = static_cast<float*>(workspace);
-  float* r = part == nullptr ? nullptr : part + 2 * static_cast<int64_t>(column_parts(M, static_cast<int>(K))) * K;
   const NormBwd a = {dy, x,     x8,      x_scale, nullptr, nullptr, gain,
-                     dx, dgain, nullptr, part,    r,       rms_eps, M, static_cast<int>(K)};
+                     dx, dgain, nullptr, static_cast<float*>(workspace), rms_eps, M, static_cast<int>(K)};
   return from_cuda(launch_norm_backward<true>(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 

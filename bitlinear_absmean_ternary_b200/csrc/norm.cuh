@@ -113,109 +113,10 @@ struct NormBwd {
   void* dx;
   float* dgain;           // or null
   float* dbias;           // or null
-  float* part;            // partial column sums
-  float* r;               // RMSNorm: r of each row, for the column sums
+  float* part;            // partial column sums: [dgain, dbias][CTA or cluster][K]
   float eps;
   int64_t M;
   int K;
 };
-
-template <typename T, bool COPY>
-BN_DEV F8 norm_load_x(const NormBwd& a, int64_t m, int c) {
-  if constexpr (COPY) return load_act8(a.x8, a.x_scale, m * (a.K >> 3) + c);
-  else return load8(static_cast<const T*>(a.x) + m * a.K + 8 * c);
-}
-
-// dx of a row: a CTA per row, two passes.
-template <typename T, bool COPY, bool RMS>
-__global__ void __launch_bounds__(kNormThreads) norm_dx_kernel(const NormBwd a) {
-  __shared__ float red[kNormThreads / 32];
-  const int64_t m = blockIdx.x;
-  const int nchunks = a.K >> 3;
-  const float invK = 1.0f / static_cast<float>(a.K);
-  const T* dy = static_cast<const T*>(a.dy) + m * a.K;
-  const T* gain = static_cast<const T*>(a.gain);
-  pdl_wait();
-  const float mean = RMS ? 0.0f : a.mean[m];
-  float s0 = 0.0f, s1 = 0.0f;
-  for (int c = threadIdx.x; c < nchunks; c += kNormThreads) {
-    const F8 d = load8(dy + 8 * c), x = norm_load_x<T, COPY>(a, m, c);
-    const F8 g = load8_or(gain, c, 1.0f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float t = d.v[e] * g.v[e];
-      const float xc = x.v[e] - mean;
-      s0 += RMS ? xc * xc : t;
-      s1 += t * xc;
-    }
-  }
-  s0 = cta_sum<kNormThreads>(s0, red);
-  s1 = cta_sum<kNormThreads>(s1, red);
-  const float r = RMS ? __fdiv_rn(1.0f, __fsqrt_rn(s0 * invK + a.eps)) : a.rstd[m];
-  const float m1 = RMS ? 0.0f : s0 * invK, m2 = s1 * r * invK;
-  for (int c = threadIdx.x; c < nchunks; c += kNormThreads) {
-    const F8 d = load8(dy + 8 * c), x = norm_load_x<T, COPY>(a, m, c);
-    const F8 g = load8_or(gain, c, 1.0f);
-    F8 o;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float t = d.v[e] * g.v[e];
-      o.v[e] = r * (t - m1 - (x.v[e] - mean) * r * m2);
-    }
-    store8(static_cast<T*>(a.dx) + m * a.K + 8 * c, o);
-  }
-  if (RMS && threadIdx.x == 0 && a.dgain != nullptr) a.r[m] = r;
-  pdl_launch_dependents();
-}
-
-// Partial column sums: CTA (j, p) sums columns 256 j .. + 255 over the rows
-// p, p + P, ...; 32 threads across the columns, 8 rows at a time.
-template <typename T, bool COPY, bool RMS>
-__global__ void __launch_bounds__(kNormThreads) norm_columns_kernel(const NormBwd a) {
-  __shared__ float red[8][256];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const int64_t P = gridDim.y;
-  pdl_wait();
-  F8 sg = {}, sb = {};
-  if (c < (a.K >> 3)) {
-    for (int64_t m = blockIdx.y * 8 + w; m < a.M; m += 8 * P) {
-      const F8 d = load8(static_cast<const T*>(a.dy) + m * a.K + 8 * c), x = norm_load_x<T, COPY>(a, m, c);
-      const float mean = RMS ? 0.0f : a.mean[m], r = RMS ? a.r[m] : a.rstd[m];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sg.v[e] += d.v[e] * ((x.v[e] - mean) * r);
-        sb.v[e] += d.v[e];
-      }
-    }
-  }
-  for (int pass = 0; pass < 2; ++pass) {
-    float* out = pass == 0 ? a.dgain : a.dbias;
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) red[w][8 * lane + e] = pass == 0 ? sg.v[e] : sb.v[e];
-    __syncthreads();
-    float s = 0.0f;
-    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-    const int k = blockIdx.x * 256 + static_cast<int>(threadIdx.x);
-    if (out != nullptr && k < a.K) a.part[(pass * P + blockIdx.y) * a.K + k] = s;
-  }
-  pdl_launch_dependents();
-}
-
-// The partial sums added in increasing order; blockIdx.y 0 is dgain, 1 dbias.
-__global__ void __launch_bounds__(kNormThreads)
-    norm_columns_join_kernel(const float* __restrict__ part, int P, int K, float* __restrict__ dgain,
-                             float* __restrict__ dbias) {
-  const int k = blockIdx.x * kNormThreads + static_cast<int>(threadIdx.x);
-  float* out = blockIdx.y == 0 ? dgain : dbias;
-  pdl_wait();
-  if (out != nullptr && k < K) {
-    float s = 0.0f;
-    for (int p = 0; p < P; ++p) s += part[(static_cast<int64_t>(blockIdx.y) * P + p) * K + k];
-    out[k] = s;
-  }
-  pdl_launch_dependents();
-}
 
 }  // namespace bitnet

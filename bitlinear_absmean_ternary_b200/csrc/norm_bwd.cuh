@@ -1,0 +1,558 @@
+// Gradients of layer norm and RMSNorm (formulas in norm.cuh) in one pass over
+// dy and x: dx row by row, and the sums over rows of dgain and dbias in
+// registers on the way.
+//
+// A team of threads (a warp, part of a CTA, a CTA or a cluster of CTAs) walks
+// the rows u, u + U, ... (U teams in all); each of its threads keeps the same
+// columns in every row, C pieces of 16 bytes, so a column's sums stay in that
+// thread's registers until the end.  Rows stream into shared memory by bulk
+// copies, a batch of R rows ahead of the batch at work.  The two sums of each
+// row of a batch are reduced together (shuffles that halve the set of values
+// first) and pass one team barrier; what else is wanted once per row is
+// computed for all rows of the batch at once, each in its lanes.  dy and x are
+// read from shared memory a second time for dx: kept in registers as fp32 they
+// leave too few warps per SM.
+//
+// In a cluster every warp sends its sums to every CTA (st.async, counted by an
+// mbarrier of the receiver), so no fence waits for the stores of dx, as the
+// cluster barrier's release would: M = 2048, K = 21504 took 108 us with that.
+//
+// At the end the teams of a CTA add their column sums in order and write one
+// partial row per CTA (cluster), which norm_join_kernel adds in order; one
+// partial row alone is the result.
+//
+// Bound by memory for many rows (K = 2560 without the column sums: 0.94 of
+// measured HBM at M = 18944, 0.72 at M = 4096; RMSNorm at M = 2048, K = 21504
+// 51.7 us, 0.79), by the two launches and the join (about 4 us) for few.
+#pragma once
+
+#include "norm.cuh"
+
+namespace bitnet {
+
+// ------------------------------------------------- pairs of fp32 values
+
+BN_DEV uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+BN_DEV float f2_lo(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+BN_DEV float f2_hi(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+BN_DEV uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+BN_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+BN_DEV uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// --------------------------------------------------------- 16-byte pieces
+
+// A piece is 16 bytes of T: V values, as V/2 pairs.
+template <typename T>
+struct Piece {
+  static constexpr int V = 16 / static_cast<int>(sizeof(T));
+  uint64_t p[V / 2];
+};
+
+BN_DEV void unpack_piece(const uint4& u, Piece<__nv_bfloat16>& r) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+BN_DEV void unpack_piece(const uint4& u, Piece<float>& r) {
+  r.p[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+  r.p[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+
+BN_DEV uint4 pack_piece(const Piece<__nv_bfloat16>& r) {
+  return make_uint4(pack_bf16x2(f2_lo(r.p[0]), f2_hi(r.p[0])), pack_bf16x2(f2_lo(r.p[1]), f2_hi(r.p[1])),
+                    pack_bf16x2(f2_lo(r.p[2]), f2_hi(r.p[2])), pack_bf16x2(f2_lo(r.p[3]), f2_hi(r.p[3])));
+}
+
+BN_DEV uint4 pack_piece(const Piece<float>& r) {
+  return make_uint4(__float_as_uint(f2_lo(r.p[0])), __float_as_uint(f2_hi(r.p[0])), __float_as_uint(f2_lo(r.p[1])),
+                    __float_as_uint(f2_hi(r.p[1])));
+}
+
+// Four codes of an 8-bit copy (act8_decode's arithmetic) as two pairs.
+BN_DEV void decode_codes4(uint32_t codes, uint64_t scale2, uint64_t* p) {
+  const uint32_t w = codes ^ 0x80808080u;
+  const uint64_t bias = f2(-8388736.0f, -8388736.0f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t v = f2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i))),
+                          __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i + 1))));
+    p[i] = f2_mul(f2_add(v, bias), scale2);
+  }
+}
+
+// ------------------------------------------------------ shared memory
+
+// Volatile: a second read is a second load, not a register kept since the first.
+BN_DEV uint4 lds128_again(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+BN_DEV uint2 lds64_again(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+BN_DEV uint32_t lds32_again(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Four values to shared memory of a CTA of the cluster, counted as 16 bytes by
+// an mbarrier there.
+BN_DEV void send_cluster(uint32_t cluster_addr, const float* v, uint32_t cluster_bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(cluster_bar)
+      : "memory");
+}
+// Barrier of one team of a CTA.
+BN_DEV void team_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// ------------------------------------------------------------ reductions
+
+// Sums of N (4 or 8) values over the warp: value i ends up in the 32 / N lanes
+// from lane i * 32 / N on.
+BN_DEV float warp_sums(const float (&v)[4], int lane) {
+  const bool h16 = lane & 16, h8 = lane & 8;
+  const float a = (h16 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, h16 ? v[0] : v[2], 16);
+  const float b = (h16 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, h16 ? v[1] : v[3], 16);
+  float k = (h8 ? b : a) + __shfl_xor_sync(0xffffffffu, h8 ? a : b, 8);
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1) k += __shfl_xor_sync(0xffffffffu, k, d);
+  return k;
+}
+BN_DEV float warp_sums(const float (&v)[8], int lane) {
+  float a[4], b[2];
+  const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    a[i] = (h16 ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, h16 ? v[i] : v[i + 4], 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    b[i] = (h8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, h8 ? a[i] : a[i + 2], 8);
+  float k = (h4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, h4 ? b[0] : b[1], 4);
+  k += __shfl_xor_sync(0xffffffffu, k, 2);
+  return k + __shfl_xor_sync(0xffffffffu, k, 1);
+}
+
+// ---------------------------------------------------------------- kernel
+
+constexpr int kNormBwdThreads = 512;  // at most
+constexpr int kNormMaxTeams = 8;      // of a CTA
+constexpr int kNormMaxWarpSums = 64;  // warps of a team over its cluster
+
+enum NormTeam { kWarpTeam, kCtaTeam, kClusterTeam };
+
+// Bytes of a row in the ring: dy, then x or its codes, each for all of the
+// team's threads (what lies past the row's columns stays zero).
+template <typename T, bool COPY, int C>
+__host__ __device__ constexpr int norm_bwd_row_bytes(int team) {
+  return team * C * (16 + (COPY ? 16 / static_cast<int>(sizeof(T)) : 16));
+}
+
+// team: threads per row and CTA (a multiple of 32; blockDim.x is a multiple of
+// it; 32 for kWarpTeam).  split: CTAs per row, the cluster size (1 but for
+// kClusterTeam).  cols: columns per CTA, a multiple of 64 (the last of a
+// cluster may have fewer).
+template <typename T, bool COPY, bool RMS, int MODE, int C, int R>
+__global__ void __launch_bounds__(kNormBwdThreads)
+    norm_bwd_kernel(const NormBwd a, int team, int split, int cols) {
+  constexpr int V = Piece<T>::V;
+  constexpr int NV = 2 * R, kLanes = 32 / NV;  // sums of a batch, lanes that hold each
+  constexpr int XB = COPY ? V : 16;            // bytes of x per piece
+  constexpr int kRed = MODE == kWarpTeam ? 4 : MODE == kCtaTeam ? NV * 16 : NV * kNormMaxWarpSums;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float red[2][kRed];  // [warp][value], teams one after the other
+  __shared__ __align__(8) uint64_t full[kNormMaxTeams][2];
+  __shared__ __align__(8) uint64_t sent[2];
+
+  const int nthr = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  const int my_team = MODE == kClusterTeam ? 0 : tid / team, t = tid - my_team * team;
+  const int nteams = MODE == kClusterTeam ? 1 : nthr / team, tw = team >> 5, warp = t >> 5;
+  const int rank = MODE == kClusterTeam ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cluster_id = static_cast<int>(MODE == kClusterTeam ? blockIdx.x / static_cast<unsigned>(split) : blockIdx.x);
+  const int clusters = static_cast<int>(MODE == kClusterTeam ? gridDim.x / static_cast<unsigned>(split) : gridDim.x);
+  const int U = clusters * nteams;
+  const int unit = cluster_id * nteams + my_team;
+  const int M = static_cast<int>(a.M);
+  const int rows = unit < M ? (M - 1 - unit) / U + 1 : 0;  // of this team: unit, unit + U, ...
+  const int col0 = rank * cols;
+  const int my_cols = a.K - col0 < cols ? a.K - col0 : cols;
+
+  // The ring of this team: two stages of R rows.
+  const int row_bytes = norm_bwd_row_bytes<T, COPY, C>(team);
+  const int x_at = team * C * 16;  // x behind dy
+  uint8_t* ring = smem + my_team * 2 * R * row_bytes;
+  uint64_t* my_full = full[my_team];
+  if (tid == 0) {
+    for (int i = 0; i < nteams; ++i) {
+      mbar_init(&full[i][0], 1);
+      mbar_init(&full[i][1], 1);
+    }
+    mbar_init(&sent[0], 1);
+    mbar_init(&sent[1], 1);
+    fence_barrier_init();
+  }
+  bool ok[C];  // piece t + j team exists; no copy writes the others' places
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    ok[j] = (t + j * team) * V < my_cols;
+    if (!ok[j]) {
+#pragma unroll 1
+      for (int r = 0; r < 2 * R; ++r) {
+        uint32_t* d = reinterpret_cast<uint32_t*>(ring + r * row_bytes + 16 * (t + j * team));
+        uint32_t* x = reinterpret_cast<uint32_t*>(ring + r * row_bytes + x_at + XB * (t + j * team));
+        d[0] = d[1] = d[2] = d[3] = 0;
+        for (int i = 0; i < XB / 4; ++i) x[i] = 0;
+      }
+    }
+  }
+  if constexpr (MODE == kClusterTeam) cluster_sync();
+  else __syncthreads();
+
+  pdl_wait();
+  // Without a join behind it the next kernel may start its own prologue now;
+  // with one, its CTAs would only take this kernel's place on the SMs
+  // (M = 4096, K = 2560: 19.0 us with the join let go here, 17.3 at the end).
+  const bool joined = clusters > 1 && (a.dgain != nullptr || a.dbias != nullptr);
+  if (!joined) pdl_launch_dependents();
+
+  const uint64_t once = policy_evict_first();
+  const int64_t step = static_cast<int64_t>(U) * a.K;
+  const int64_t first = static_cast<int64_t>(unit) * a.K + col0;
+  auto fill = [&](int row, int stage) {  // one thread of the team: rows row .. row + R - 1
+    const int n = rows - row < R ? rows - row : R;
+    const uint32_t bytes = static_cast<uint32_t>(my_cols * static_cast<int>(sizeof(T)));
+    const uint32_t xbytes = COPY ? static_cast<uint32_t>(my_cols) : bytes;
+    mbar_arrive_expect_tx(&my_full[stage], static_cast<uint32_t>(n) * (bytes + xbytes));
+#pragma unroll 1
+    for (int r = 0; r < n; ++r) {
+      const int64_t at = first + static_cast<int64_t>(row + r) * step;
+      uint8_t* to = ring + (stage * R + r) * row_bytes;
+      bulk_copy_g2s(to, static_cast<const T*>(a.dy) + at, bytes, &my_full[stage], once);
+      if constexpr (COPY) bulk_copy_g2s(to + x_at, a.x8 + at, xbytes, &my_full[stage], once);
+      else bulk_copy_g2s(to + x_at, static_cast<const T*>(a.x) + at, xbytes, &my_full[stage], once);
+    }
+  };
+  if (t == 0) {
+    if (rows > 0) fill(0, 0);
+    if (rows > R) fill(R, 1);
+  }
+
+  Piece<T> gain[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const uint32_t one = sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u;
+    unpack_piece(a.gain != nullptr && ok[j] ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.gain) + col0 +
+                                                                                   (t + j * team) * V))
+                                            : make_uint4(one, one, one, one),
+                 gain[j]);
+  }
+
+  // Of the next batch: layer norm's statistics, row r's in the lanes of its
+  // sums, and the scales of the 8-bit copy.
+  const int lane_row = lane / (2 * kLanes);
+  float mean_n = 0.0f, rstd_n = 0.0f, scale_n[COPY ? R : 1][C];
+  auto fetch_small = [&](int row) {
+    if constexpr (!RMS) {
+      const bool live = row + lane_row < rows;
+      const int64_t m = unit + static_cast<int64_t>(row + lane_row) * U;
+      mean_n = live ? __ldg(a.mean + m) : 0.0f;
+      rstd_n = live ? __ldg(a.rstd + m) : 0.0f;
+    }
+    if constexpr (COPY) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool live = row + r < rows;
+        const float* p = a.x_scale + (first + static_cast<int64_t>(row + r) * step) / kAct8Group;
+#pragma unroll
+        for (int j = 0; j < C; ++j) scale_n[r][j] = live && ok[j] ? __ldg(p + (t + j * team) * V / kAct8Group) : 0.0f;
+      }
+    }
+  };
+  fetch_small(0);
+
+  uint64_t acc_g[C][V / 2], acc_b[C][V / 2];
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) acc_g[j][i] = acc_b[j][i] = 0;
+
+  // dy and x of piece j of a row in the ring; s: its scale
+  const uint32_t my_dy = smem_addr(ring) + 16 * t, my_x = smem_addr(ring) + x_at + XB * t;
+  auto values = [&](int row_at, int j, float s, Piece<T>& d, Piece<T>& x) {
+    unpack_piece(lds128_again(my_dy + row_at + 16 * j * team), d);
+    const uint32_t at = my_x + row_at + XB * j * team;
+    if constexpr (!COPY) {
+      unpack_piece(lds128_again(at), x);
+    } else {
+      const uint64_t s2 = f2(s, s);
+      if constexpr (V == 8) {
+        const uint2 q = lds64_again(at);
+        decode_codes4(q.x, s2, x.p);
+        decode_codes4(q.y, s2, x.p + 2);
+      } else {
+        decode_codes4(lds32_again(at), s2, x.p);
+      }
+    }
+  };
+
+  const float inv_k = 1.0f / static_cast<float>(a.K);
+  const int val = lane / kLanes, e0 = lane % kLanes;
+  T* dx = static_cast<T*>(a.dx) + first + t * V;
+  int dead = -1;  // the batch at which a wait gave up: no more waits or fills, the results are lost
+  int b = 0;      // the batch; its parity is its stage
+  for (int row = 0; row < rows; row += R, ++b) {
+    const float rstd = rstd_n, shift = -mean_n * rstd_n;
+    float scale[COPY ? R : 1][C];
+    if constexpr (COPY) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < C; ++j) scale[r][j] = scale_n[r][j];
+    }
+    fetch_small(row + R);
+    if (dead < 0 && !mbar_wait(&my_full[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
+    const int base = (b & 1) * R * row_bytes;
+
+    float sums[NV];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sums[2 * r] = sums[2 * r + 1] = 0.0f;
+      if (r == 0 || row + r < rows) {
+        const float rr = RMS ? 0.0f : __shfl_sync(0xffffffffu, rstd, 2 * kLanes * r);
+        const float cc = RMS ? 0.0f : __shfl_sync(0xffffffffu, shift, 2 * kLanes * r);
+        const uint64_t r2 = f2(rr, rr), c2 = f2(cc, cc);
+        uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          Piece<T> d, x;
+          values(base + r * row_bytes, j, COPY ? scale[COPY ? r : 0][j] : 0.0f, d, x);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            const uint64_t tt = f2_mul(d.p[i], gain[j].p[i]);
+            if constexpr (RMS) {
+              s0 = f2_fma(x.p[i], x.p[i], s0);
+              s1 = f2_fma(tt, x.p[i], s1);
+            } else {
+              const uint64_t nn = f2_fma(x.p[i], r2, c2);
+              s0 = f2_add(s0, tt);
+              s1 = f2_fma(tt, nn, s1);
+              acc_g[j][i] = f2_fma(d.p[i], nn, acc_g[j][i]);
+              acc_b[j][i] = f2_add(acc_b[j][i], d.p[i]);
+            }
+          }
+        }
+        sums[2 * r] = f2_lo(s0) + f2_hi(s0);
+        sums[2 * r + 1] = f2_lo(s1) + f2_hi(s1);
+      }
+    }
+
+    // the team's sums: value i in the kLanes lanes from i * kLanes on
+    float k = warp_sums(sums, lane);
+    if constexpr (MODE != kWarpTeam) {
+      float* buf = &red[b & 1][MODE == kCtaTeam ? my_team * tw * NV : 0];
+      int entries = tw;
+      if constexpr (MODE == kCtaTeam) {
+        if (e0 == 0) buf[warp * NV + val] = k;
+        team_sync(1 + my_team, team);
+      } else {
+        entries = split * tw;
+        float mine[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) mine[i] = __shfl_sync(0xffffffffu, k, i * kLanes);
+        if (tid == 0) mbar_arrive_expect_tx(&sent[b & 1], static_cast<uint32_t>(entries * NV * 4));
+        if (lane < split) {
+          const uint32_t to = mapa_shared(smem_addr(buf + (rank * tw + warp) * NV), lane);
+          const uint32_t bar = mapa_shared(smem_addr(&sent[b & 1]), lane);
+#pragma unroll
+          for (int i = 0; i < NV; i += 4) send_cluster(to + 4 * i, mine + i, bar);
+        }
+        if (dead < 0 && !mbar_wait_cluster(&sent[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
+      }
+      k = 0.0f;
+#pragma unroll 1
+      for (int e = e0; e < entries; e += kLanes) k += buf[e * NV + val];
+#pragma unroll
+      for (int d = kLanes / 2; d >= 1; d >>= 1) k += __shfl_xor_sync(0xffffffffu, k, d);
+    }
+
+    // Lanes of value 2 r: row r's dx = r t + n B + A = r t + x (r B) + (shift B + A),
+    //   RMSNorm     B = -r (r s1 / K), A = 0 (s1 is of t x, and dx = r t + n B is used)
+    //   layer norm  B = -r s1 / K,     A = -r s0 / K
+    const float k1 = __shfl_xor_sync(0xffffffffu, k, kLanes);
+    float row_r, row_a = 0.0f, row_b;
+    if constexpr (RMS) {
+      row_r = __fdiv_rn(1.0f, __fsqrt_rn(k * inv_k + a.eps));
+      row_b = -row_r * (row_r * k1 * inv_k);
+    } else {
+      row_r = rstd;
+      row_b = -rstd * (k1 * inv_k);
+      row_a = shift * row_b - rstd * (k * inv_k);
+      row_b *= rstd;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r == 0 || row + r < rows) {
+        const float rr = __shfl_sync(0xffffffffu, row_r, 2 * kLanes * r);
+        const float bb = __shfl_sync(0xffffffffu, row_b, 2 * kLanes * r);
+        const float aa = RMS ? 0.0f : __shfl_sync(0xffffffffu, row_a, 2 * kLanes * r);
+        const uint64_t r2 = f2(rr, rr), a2 = f2(aa, aa), b2 = f2(bb, bb);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          Piece<T> d, x, o;
+          values(base + r * row_bytes, j, COPY ? scale[COPY ? r : 0][j] : 0.0f, d, x);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            const uint64_t tt = f2_mul(d.p[i], gain[j].p[i]);
+            if constexpr (RMS) {
+              const uint64_t nn = f2_mul(x.p[i], r2);
+              acc_g[j][i] = f2_fma(nn, d.p[i], acc_g[j][i]);
+              o.p[i] = f2_fma(tt, r2, f2_mul(nn, b2));
+            } else {
+              o.p[i] = f2_fma(tt, r2, f2_fma(x.p[i], b2, a2));
+            }
+          }
+          if (ok[j]) *reinterpret_cast<uint4*>(dx + j * team * V) = pack_piece(o);
+        }
+        dx += step;
+      }
+    }
+
+    // every thread of the team is done with the stage
+    if constexpr (MODE == kWarpTeam) __syncwarp();
+    else team_sync(1 + my_team, team);
+    if (t == 0 && row + 2 * R < rows && dead < 0) {
+      fence_proxy_async_smem();
+      fill(row + 2 * R, b & 1);
+    }
+  }
+  // After a timeout: the copies still in flight land before shared memory goes away.
+  if (dead >= 0 && t == 0)
+    for (int i = dead; i < dead + 2 && i * R < rows; ++i) mbar_wait(&my_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u);
+  if constexpr (MODE == kClusterTeam) cluster_sync();  // nothing more is sent to a CTA that has ended
+
+  if (a.dgain == nullptr && a.dbias == nullptr) return;
+  // The teams' column sums, added in order: teams 1, 2, ... leave theirs in
+  // shared memory, [team - 1][array][column], and team 0 adds and writes.
+  float* tsum = reinterpret_cast<float*>(smem);
+  if (nteams > 1) {
+    __syncthreads();
+    if (my_team > 0) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        if (!ok[j]) continue;
+        float* p = tsum + (my_team - 1) * 2 * cols + (t + j * team) * V;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          *reinterpret_cast<uint64_t*>(p + 2 * i) = acc_g[j][i];
+          if constexpr (!RMS) *reinterpret_cast<uint64_t*>(p + cols + 2 * i) = acc_b[j][i];
+        }
+      }
+    }
+    __syncthreads();
+    if (my_team > 0) return;
+  }
+  float* out_g = clusters == 1 ? a.dgain : a.part + static_cast<int64_t>(cluster_id) * a.K;
+  float* out_b = clusters == 1 ? a.dbias : a.part + static_cast<int64_t>(clusters + cluster_id) * a.K;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    if (!ok[j]) continue;
+#pragma unroll 1
+    for (int i = 1; i < nteams; ++i) {
+      const float* p = tsum + (i - 1) * 2 * cols + (t + j * team) * V;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        acc_g[j][e] = f2_add(acc_g[j][e], *reinterpret_cast<const uint64_t*>(p + 2 * e));
+        if constexpr (!RMS) acc_b[j][e] = f2_add(acc_b[j][e], *reinterpret_cast<const uint64_t*>(p + cols + 2 * e));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      if (a.dgain != nullptr)
+        *reinterpret_cast<ulonglong2*>(out_g + col0 + (t + j * team) * V + 4 * i) = make_ulonglong2(acc_g[j][2 * i], acc_g[j][2 * i + 1]);
+      if constexpr (!RMS)
+        if (a.dbias != nullptr)
+          *reinterpret_cast<ulonglong2*>(out_b + col0 + (t + j * team) * V + 4 * i) = make_ulonglong2(acc_b[j][2 * i], acc_b[j][2 * i + 1]);
+    }
+  }
+  pdl_launch_dependents();
+}
+
+// Shared memory of a CTA: the rings, reused for the teams' column sums.
+template <typename T, bool COPY, int C, int R>
+inline int norm_bwd_smem_bytes(int teams, int team, int cols) {
+  const int ring = teams * 2 * R * norm_bwd_row_bytes<T, COPY, C>(team);
+  const int sums = (teams - 1) * 2 * cols * 4;
+  return ring > sums ? ring : sums;
+}
+
+// The P partial rows added in a fixed order: a CTA takes 32 columns (8 lanes
+// of 4), its 32 groups of 8 lanes every 32nd partial row each, and adds the
+// groups' sums in order.  blockIdx.y 0 is dgain, 1 dbias.
+constexpr int kNormJoinThreads = 256;
+constexpr int kNormJoinLanes = 8;
+constexpr int kNormJoinLoads = 5;  // in flight per thread
+
+__global__ void __launch_bounds__(kNormJoinThreads)
+    norm_join_kernel(const float* __restrict__ part, int P, int K, float* __restrict__ dgain,
+                     float* __restrict__ dbias) {
+  constexpr int G = kNormJoinThreads / kNormJoinLanes, W = 4 * kNormJoinLanes;
+  __shared__ float4 sums[G][kNormJoinLanes];
+  const int q = threadIdx.x % kNormJoinLanes, grp = threadIdx.x / kNormJoinLanes;
+  const int col = (blockIdx.x * kNormJoinLanes + q) * 4;  // K is a multiple of 64
+  float* out = blockIdx.y == 0 ? dgain : dbias;
+  pdl_wait();
+  if (out != nullptr) {
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float* base = part + static_cast<int64_t>(blockIdx.y) * P * K + col;
+    for (int p = grp; p < P; p += G * kNormJoinLoads) {
+      float4 v[kNormJoinLoads];
+#pragma unroll
+      for (int i = 0; i < kNormJoinLoads; ++i)
+        v[i] = p + G * i < P ? __ldcg(reinterpret_cast<const float4*>(base + static_cast<int64_t>(p + G * i) * K))
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kNormJoinLoads; ++i) {
+        s.x += v[i].x;
+        s.y += v[i].y;
+        s.z += v[i].z;
+        s.w += v[i].w;
+      }
+    }
+    sums[grp][q] = s;
+    __syncthreads();
+    if (threadIdx.x < W) {
+      const float* f = reinterpret_cast<const float*>(sums);
+      float t[4] = {};
+#pragma unroll
+      for (int i = 0; i < G; ++i) t[i & 3] += f[i * W + threadIdx.x];
+      out[blockIdx.x * W + threadIdx.x] = (t[0] + t[1]) + (t[2] + t[3]);
+    }
+  }
+  pdl_launch_dependents();
+}
+
+}  // namespace bitnet
