@@ -546,71 +546,96 @@ ACT8_GROUP = 64  # columns of a row that share a scale in an 8-bit copy
 def _launch(name: str, device, *args) -> None:
     """Calls an entry point on the current stream of `device`, with that device current."""
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        st = getattr(lib(), name)(*args, _stream(device))
+    index = device.index
+    if torch.cuda.current_device() == index:
+        st = getattr(lib(), name)(*args, _stream(index))
     else:
-        with torch.cuda.device(device):
-            st = getattr(lib(), name)(*args, _stream(device))
+        with torch.cuda.device(index):
+            st = getattr(lib(), name)(*args, _stream(index))
     if st != BITNET_OK:
         raise BitnetError(name, st)
 
 
 def _matrix(name: str, t):
-    """Rows, columns, dtype, dtype code and device of a contiguous M x K float tensor on a CUDA device."""
-    _need_cuda(t)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
-    code = _dtype_code(t.dtype)
+    """Shape, dtype, dtype code and device of a contiguous M x K float tensor on a CUDA device."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    shape, dt = t.shape, t.dtype
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {len(shape)} dimensions")
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    code = _dtype_code(dt)
     if code == BITNET_I32:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    return t.shape[0], t.shape[1], t.dtype, code, t.device
+    return shape, dt, code, t.device
 
 
-def _expect(name: str, t, shape, dtype, device):
-    """Refuses a tensor that does not have this shape, type and device; None passes."""
-    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+def _expect(name: str, t, shape, dtype, device) -> int:
+    """Address of a tensor that has to have this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _maybe(name: str, t, shape, dtype, device):
+    """As _expect, None for None."""
+    return None if t is None else _expect(name, t, shape, dtype, device)
+
+
+def _like(name: str, t, x, shape, dtype, device):
+    """The caller's output of x's shape and type, checked, or a new one."""
+    if t is None:
+        return _torch().empty_like(x)
+    _expect(name, t, shape, dtype, device)
     return t
 
 
-def _output(name: str, t, shape, dtype, device):
-    """The caller's output tensor, checked, or a new one."""
+def _output(name: str, t, x, shape, dtype, device):
+    """The caller's output, checked, or a new one on x's device."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    return _expect(name, t, shape, dtype, device)
+        return x.new_empty(shape, dtype=dtype)
+    _expect(name, t, shape, dtype, device)
+    return t
 
 
-def _copy_of(name: str, x8, x_scale, M: int, K: int, device) -> None:
-    """Checks an 8-bit copy of an M x K activation that a call reads."""
+def _copy_of(name: str, x8, x_scale, shape, device):
+    """Addresses of the 8-bit copy of an M x K activation that a call reads."""
     torch = _torch()
     if x8 is None or x_scale is None:
         raise ValueError(f"the 8-bit copy of {name} needs its codes and its scales")
-    _expect(f"{name}8", x8, (M, K), torch.int8, device)
-    _expect(f"{name}_scale", x_scale, (M, K // ACT8_GROUP), torch.float32, device)
+    return (_expect(f"{name}8", x8, shape, torch.int8, device),
+            _expect(f"{name}_scale", x_scale, (shape[0], shape[1] // ACT8_GROUP), torch.float32, device))
+
+
+def _copy_out(name: str, x8, x_scale, x, shape, device):
+    """The caller's buffers for an 8-bit copy, checked, or new ones."""
+    torch = _torch()
+    return (_output(f"{name}8", x8, x, shape, torch.int8, device),
+            _output(f"{name}_scale", x_scale, x, (shape[0], shape[1] // ACT8_GROUP), torch.float32, device))
 
 
 def bitnet_act_checkpoint(x, x8=None, x_scale=None):
     """x (M x K float32 or bfloat16) in 8 bits for the backward pass: int8 codes
     and one float32 scale per row and 64 columns.  Returns (x8, x_scale)."""
-    torch = _torch()
-    M, K, _, code, dev = _matrix("x", x)
-    x8 = _output("x8", x8, (M, K), torch.int8, dev)
-    x_scale = _output("x_scale", x_scale, (M, K // ACT8_GROUP), torch.float32, dev)
-    _launch("bitnet_act_checkpoint", dev, _ptr(x), code, M, K, _ptr(x8), _ptr(x_scale))
+    shape, _, code, dev = _matrix("x", x)
+    x8, x_scale = _copy_out("x", x8, x_scale, x, shape, dev)
+    _launch("bitnet_act_checkpoint", dev, x.data_ptr(), code, shape[0], shape[1], x8.data_ptr(), x_scale.data_ptr())
     return x8, x_scale
 
 
 def bitnet_act_restore(x8, x_scale, out_dtype=None, x=None):
     """The values of an 8-bit copy as an M x K tensor of out_dtype (bfloat16 by default)."""
     torch = _torch()
-    _need_cuda(x8)
-    if x8.dim() != 2:
+    if not x8.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    shape, dev = x8.shape, x8.device
+    if len(shape) != 2:
         raise ValueError("x8 must be a matrix")
-    (M, K), dev = x8.shape, x8.device
-    _copy_of("x", x8, x_scale, M, K, dev)
-    x = _output("x", x, (M, K), out_dtype or (torch.bfloat16 if x is None else x.dtype), dev)
-    _launch("bitnet_act_restore", dev, _ptr(x8), _ptr(x_scale), M, K, _ptr(x), _dtype_code(x.dtype))
+    p8, ps = _copy_of("x", x8, x_scale, shape, dev)
+    x = _output("x", x, x8, shape, out_dtype or (torch.bfloat16 if x is None else x.dtype), dev)
+    _launch("bitnet_act_restore", dev, p8, ps, shape[0], shape[1], x.data_ptr(), _dtype_code(x.dtype))
     return x
 
 
@@ -619,21 +644,24 @@ def bitnet_layernorm(x, gain=None, bias=None, eps: float = 1e-5, checkpoint: boo
     """Layer norm of the rows of x (M x K float32 or bfloat16); gain and bias: K
     values of x's type, or None.  Returns (y, mean, rstd), and with checkpoint
     also x's 8-bit copy, written in the same pass: (y, mean, rstd, x8, x_scale)."""
-    torch = _torch()
-    M, K, dt, code, dev = _matrix("x", x)
-    _expect("gain", gain, (K,), dt, dev)
-    _expect("bias", bias, (K,), dt, dev)
-    y = _output("y", y, (M, K), dt, dev)
-    mean = _output("mean", mean, (M,), torch.float32, dev)
-    rstd = _output("rstd", rstd, (M,), torch.float32, dev)
+    shape, dt, code, dev = _matrix("x", x)
+    M, K = shape
+    pg = _maybe("gain", gain, (K,), dt, dev)
+    pb = _maybe("bias", bias, (K,), dt, dev)
+    y = _like("y", y, x, shape, dt, dev)
+    f32 = _torch().float32
+    mean = _output("mean", mean, x, (M,), f32, dev)
+    rstd = _output("rstd", rstd, x, (M,), f32, dev)
     if checkpoint:
-        x8 = _output("x8", x8, (M, K), torch.int8, dev)
-        x_scale = _output("x_scale", x_scale, (M, K // ACT8_GROUP), torch.float32, dev)
-    elif x8 is not None or x_scale is not None:
+        x8, x_scale = _copy_out("x", x8, x_scale, x, shape, dev)
+        _launch("bitnet_layernorm", dev, x.data_ptr(), code, M, K, pg, pb, eps, y.data_ptr(), mean.data_ptr(),
+                rstd.data_ptr(), x8.data_ptr(), x_scale.data_ptr())
+        return y, mean, rstd, x8, x_scale
+    if x8 is not None or x_scale is not None:
         raise ValueError("x8 and x_scale are outputs of checkpoint=True")
-    _launch("bitnet_layernorm", dev, _ptr(x), code, M, K, _ptr(gain), _ptr(bias), eps, _ptr(y), _ptr(mean),
-            _ptr(rstd), _ptr(x8), _ptr(x_scale))
-    return (y, mean, rstd, x8, x_scale) if checkpoint else (y, mean, rstd)
+    _launch("bitnet_layernorm", dev, x.data_ptr(), code, M, K, pg, pb, eps, y.data_ptr(), mean.data_ptr(),
+            rstd.data_ptr(), None, None)
+    return y, mean, rstd
 
 
 def bitnet_norm_backward_workspace_bytes(M: int, K: int) -> int:
@@ -641,30 +669,32 @@ def bitnet_norm_backward_workspace_bytes(M: int, K: int) -> int:
     return int(lib().bitnet_norm_backward_workspace_bytes(M, K))
 
 
-def _norm_backward_args(dy, x, x8, x_scale, gain, dx, want, workspace):
-    """The checks and buffers that both norms' backward passes share."""
-    torch = _torch()
-    M, K, dt, code, dev = _matrix("dy", dy)
-    if (x is None) == (x8 is None):
-        raise ValueError("give x, or its 8-bit copy as x8 and x_scale")
+def _norm_input(x, x8, x_scale, shape, dtype, device):
+    """Addresses of x, or of its 8-bit copy: (x, x8, x_scale), None where not given."""
     if x is None:
-        _copy_of("x", x8, x_scale, M, K, dev)
-    else:
-        if x_scale is not None:
-            raise ValueError("x_scale belongs to x8")
-        _expect("x", x, (M, K), dt, dev)
-    _expect("gain", gain, (K,), dt, dev)
-    dx = _output("dx", dx, (M, K), dt, dev)
-    if want and workspace is None:
-        with torch.cuda.device(dev):
-            nbytes = bitnet_norm_backward_workspace_bytes(M, K)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    elif workspace is not None:
-        _need_cuda(workspace)
-        if workspace.device != dev:
-            raise ValueError(f"workspace must live on {dev}")
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return M, K, code, dev, dx, workspace, wsb
+        if x8 is None:
+            raise ValueError("give x, or its 8-bit copy as x8 and x_scale")
+        return (None,) + _copy_of("x", x8, x_scale, shape, device)
+    if x8 is not None or x_scale is not None:
+        raise ValueError("give x, or its 8-bit copy as x8 and x_scale")
+    return _expect("x", x, shape, dtype, device), None, None
+
+
+def _norm_workspace(workspace, dy, shape, device):
+    """Address and bytes of the caller's workspace, or of a new one (returned too, to keep it)."""
+    torch = _torch()
+    if workspace is None:
+        if torch.cuda.current_device() == device.index:
+            nbytes = bitnet_norm_backward_workspace_bytes(*shape)
+        else:
+            with torch.cuda.device(device.index):
+                nbytes = bitnet_norm_backward_workspace_bytes(*shape)
+        workspace = dy.new_empty(nbytes, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), nbytes
+    _need_cuda(workspace)
+    if workspace.device != device:
+        raise ValueError(f"workspace must live on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def bitnet_layernorm_backward(dy, mean, rstd, x=None, x8=None, x_scale=None, gain=None, dx=None, dgain=None,
@@ -675,16 +705,22 @@ def bitnet_layernorm_backward(dy, mean, rstd, x=None, x8=None, x_scale=None, gai
     workspace: a uint8 device tensor of bitnet_norm_backward_workspace_bytes
     bytes, reused across calls on one stream (allocated for this call when None)."""
     torch = _torch()
-    M, K, code, dev, dx, workspace, wsb = _norm_backward_args(dy, x, x8, x_scale, gain, dx,
-                                                              want_dgain or want_dbias, workspace)
+    shape, dt, code, dev = _matrix("dy", dy)
+    M, K = shape
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward pass are needed")
-    _expect("mean", mean, (M,), torch.float32, dev)
-    _expect("rstd", rstd, (M,), torch.float32, dev)
-    dgain = _output("dgain", dgain, (K,), torch.float32, dev) if want_dgain else None
-    dbias = _output("dbias", dbias, (K,), torch.float32, dev) if want_dbias else None
-    _launch("bitnet_layernorm_backward", dev, _ptr(dy), code, M, K, _ptr(x), _ptr(x8), _ptr(x_scale), _ptr(mean),
-            _ptr(rstd), _ptr(gain), _ptr(dx), _ptr(dgain), _ptr(dbias), _ptr(workspace), wsb)
+    px, p8, ps = _norm_input(x, x8, x_scale, shape, dt, dev)
+    pm = _expect("mean", mean, (M,), torch.float32, dev)
+    pr = _expect("rstd", rstd, (M,), torch.float32, dev)
+    pg = _maybe("gain", gain, (K,), dt, dev)
+    dx = _like("dx", dx, dy, shape, dt, dev)
+    wp = wsb = None
+    dgain = _output("dgain", dgain, dy, (K,), torch.float32, dev) if want_dgain else None
+    dbias = _output("dbias", dbias, dy, (K,), torch.float32, dev) if want_dbias else None
+    if want_dgain or want_dbias:
+        workspace, wp, wsb = _norm_workspace(workspace, dy, shape, dev)
+    _launch("bitnet_layernorm_backward", dev, dy.data_ptr(), code, M, K, px, p8, ps, pm, pr, pg, dx.data_ptr(),
+            _ptr(dgain), _ptr(dbias), wp, wsb or 0)
     return dx, dgain, dbias
 
 
@@ -695,10 +731,17 @@ def bitnet_rmsnorm_backward(dy, x=None, x8=None, x_scale=None, gain=None, rms_ep
     (dx, dgain): dx of dy's type, dgain float32 [K] or None where not wanted.
     workspace: as in bitnet_layernorm_backward."""
     torch = _torch()
-    M, K, code, dev, dx, workspace, wsb = _norm_backward_args(dy, x, x8, x_scale, gain, dx, want_dgain, workspace)
-    dgain = _output("dgain", dgain, (K,), torch.float32, dev) if want_dgain else None
-    _launch("bitnet_rmsnorm_backward", dev, _ptr(dy), code, M, K, _ptr(x), _ptr(x8), _ptr(x_scale), _ptr(gain),
-            rms_eps, _ptr(dx), _ptr(dgain), _ptr(workspace), wsb)
+    shape, dt, code, dev = _matrix("dy", dy)
+    M, K = shape
+    px, p8, ps = _norm_input(x, x8, x_scale, shape, dt, dev)
+    pg = _maybe("gain", gain, (K,), dt, dev)
+    dx = _like("dx", dx, dy, shape, dt, dev)
+    wp = wsb = None
+    dgain = _output("dgain", dgain, dy, (K,), torch.float32, dev) if want_dgain else None
+    if want_dgain:
+        workspace, wp, wsb = _norm_workspace(workspace, dy, shape, dev)
+    _launch("bitnet_rmsnorm_backward", dev, dy.data_ptr(), code, M, K, px, p8, ps, pg, rms_eps, dx.data_ptr(),
+            _ptr(dgain), wp, wsb or 0)
     return dx, dgain
 
 
@@ -706,40 +749,39 @@ def bitnet_relu2_gate(u, g, checkpoint: bool = False, h=None, u8=None, u_scale=N
     """h = relu(g)^2 * u (M x F, the type of u and g).  Returns h, and with
     checkpoint also the 8-bit copies of u and g, written in the same pass:
     (h, u8, u_scale, g8, g_scale)."""
-    torch = _torch()
-    M, F, dt, code, dev = _matrix("u", u)
-    _expect("g", g, (M, F), dt, dev)
-    h = _output("h", h, (M, F), dt, dev)
+    shape, dt, code, dev = _matrix("u", u)
+    pg = _expect("g", g, shape, dt, dev)
+    h = _like("h", h, u, shape, dt, dev)
     if checkpoint:
-        u8 = _output("u8", u8, (M, F), torch.int8, dev)
-        g8 = _output("g8", g8, (M, F), torch.int8, dev)
-        u_scale = _output("u_scale", u_scale, (M, F // ACT8_GROUP), torch.float32, dev)
-        g_scale = _output("g_scale", g_scale, (M, F // ACT8_GROUP), torch.float32, dev)
-    elif not (u8 is None and u_scale is None and g8 is None and g_scale is None):
+        u8, u_scale = _copy_out("u", u8, u_scale, u, shape, dev)
+        g8, g_scale = _copy_out("g", g8, g_scale, g, shape, dev)
+        _launch("bitnet_relu2_gate", dev, u.data_ptr(), pg, code, shape[0], shape[1], h.data_ptr(), u8.data_ptr(),
+                u_scale.data_ptr(), g8.data_ptr(), g_scale.data_ptr())
+        return h, u8, u_scale, g8, g_scale
+    if not (u8 is None and u_scale is None and g8 is None and g_scale is None):
         raise ValueError("u8, u_scale, g8 and g_scale are outputs of checkpoint=True")
-    _launch("bitnet_relu2_gate", dev, _ptr(u), _ptr(g), code, M, F, _ptr(h), _ptr(u8), _ptr(u_scale), _ptr(g8),
-            _ptr(g_scale))
-    return (h, u8, u_scale, g8, g_scale) if checkpoint else h
+    _launch("bitnet_relu2_gate", dev, u.data_ptr(), pg, code, shape[0], shape[1], h.data_ptr(), None, None, None, None)
+    return h
 
 
 def bitnet_relu2_gate_backward(dh, u=None, g=None, u8=None, u_scale=None, g8=None, g_scale=None, du=None, dg=None):
     """Gradients of the squared-ReLU gate from dh (M x F) and u and g, or their
     8-bit copies.  Returns (du, dg), of dh's type."""
-    M, F, dt, code, dev = _matrix("dh", dh)
-    if u8 is None and g8 is None:
-        if u is None or g is None or u_scale is not None or g_scale is not None:
+    shape, dt, code, dev = _matrix("dh", dh)
+    pu = pg = p8u = psu = p8g = psg = None
+    if u8 is None and g8 is None and u_scale is None and g_scale is None:
+        if u is None or g is None:
             raise ValueError("give u and g, or their 8-bit copies")
-        _expect("u", u, (M, F), dt, dev)
-        _expect("g", g, (M, F), dt, dev)
+        pu, pg = _expect("u", u, shape, dt, dev), _expect("g", g, shape, dt, dev)
     else:
         if u is not None or g is not None:
             raise ValueError("give u and g, or their 8-bit copies")
-        _copy_of("u", u8, u_scale, M, F, dev)
-        _copy_of("g", g8, g_scale, M, F, dev)
-    du = _output("du", du, (M, F), dt, dev)
-    dg = _output("dg", dg, (M, F), dt, dev)
-    _launch("bitnet_relu2_gate_backward", dev, _ptr(dh), code, M, F, _ptr(u), _ptr(g), _ptr(u8), _ptr(u_scale),
-            _ptr(g8), _ptr(g_scale), _ptr(du), _ptr(dg))
+        p8u, psu = _copy_of("u", u8, u_scale, shape, dev)
+        p8g, psg = _copy_of("g", g8, g_scale, shape, dev)
+    du = _like("du", du, dh, shape, dt, dev)
+    dg = _like("dg", dg, dh, shape, dt, dev)
+    _launch("bitnet_relu2_gate_backward", dev, dh.data_ptr(), code, shape[0], shape[1], pu, pg, p8u, psu, p8g, psg,
+            du.data_ptr(), dg.data_ptr())
     return du, dg
 
 
