@@ -1,8 +1,8 @@
 // Host side of layer norm and of the backward passes of layer norm and
 // RMSNorm (norm.cuh).
 #include "host_common.h"
-#include "norm.cuh"
 #include "norm_bwd.cuh"
+#include "norm_fwd.cuh"
 
 #include <algorithm>
 
@@ -27,23 +27,26 @@ constexpr int kNormClusterThreads = 256;
 constexpr int kNormCtasPerSm = 1;
 constexpr int kNormClusterCtasPerSm = 4;
 constexpr int kSmemPerSm = 233472;  // 228 KB
-constexpr int kNormBwdSmemMax = 220 * 1024;
+constexpr int kNormSmemMax = 220 * 1024;
 
 bool valid_rows(int64_t M, int64_t K) { return valid_k(K) && K <= kNormMaxK && M >= 1 && M <= INT32_MAX; }
 
 bool valid_eps(float eps) { return std::isfinite(eps) && eps > 0.0f; }
 
-template <typename T>
-cudaError_t launch_layernorm(const void* x, int64_t M, int K, const void* gain, const void* bias, float eps, void* y,
-                             float* mean, float* rstd, int8_t* x8, float* x_scale, cudaStream_t s) {
-  auto kern = x8 != nullptr ? layernorm_kernel<T, true> : layernorm_kernel<T, false>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(M)), dim3(kNormThreads), 0, s, static_cast<const T*>(x), K,
-                    static_cast<const T*>(gain), static_cast<const T*>(bias), eps, static_cast<T*>(y), mean, rstd, x8,
-                    x_scale);
+template <typename F>
+int kernel_registers(F* fn, std::atomic<int> (&cache)[kMaxDevices]) {
+  const int d = current_device();
+  int n = d >= 0 && d < kMaxDevices ? cache[d].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaFuncAttributes fa;
+    n = cudaFuncGetAttributes(&fa, fn) == cudaSuccess ? fa.numRegs : 128;
+    if (d >= 0 && d < kMaxDevices) cache[d].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
-// How the columns of a backward pass are dealt out: independent of the types,
-// as the workspace follows from it.
+// How the columns of a row are dealt out: independent of the types, as the
+// backward passes' workspace follows from it.
 struct NormPlan {
   int cv;     // columns per thread
   int split;  // CTAs (a cluster) per row
@@ -68,18 +71,6 @@ int64_t norm_most_parts(const NormPlan& p, int64_t M) {
   return std::min<int64_t>(M, ctas / p.split);
 }
 
-template <typename F>
-int kernel_registers(F* fn, std::atomic<int> (&cache)[kMaxDevices]) {
-  const int d = current_device();
-  int n = d >= 0 && d < kMaxDevices ? cache[d].load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    cudaFuncAttributes fa;
-    n = cudaFuncGetAttributes(&fa, fn) == cudaSuccess ? fa.numRegs : 128;
-    if (d >= 0 && d < kMaxDevices) cache[d].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 // Clusters of this launch that run at the same time (GPCs hold a whole number
 // of them, so it can be less than the SMs would suggest); the last answer is
 // kept per kernel and device as (key << 16 | answer).
@@ -97,44 +88,79 @@ int64_t active_clusters(F* fn, const cudaLaunchConfig_t& cfg, int split, std::at
   return n;
 }
 
-template <typename T, bool COPY, bool RMS, int MODE, int C, int R>
-cudaError_t launch_norm_bwd(const NormBwd& a, const NormPlan& p, cudaStream_t s) {
-  static std::atomic<bool> done[kMaxDevices] = {};
-  static std::atomic<int> regs[kMaxDevices] = {};
-  auto kern = norm_bwd_kernel<T, COPY, RMS, MODE, C, R>;
-  int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(kNormMaxTeams, kNormBwdThreads / p.team));
-  while (teams > 1 && norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols) > kNormBwdSmemMax) --teams;
-  const int threads = teams * p.team;
-  const int smem = norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols);
-  cudaError_t e = set_smem(kern, kNormBwdSmemMax, done);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.split));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
+// Grid of a kernel with a team per row: at most `most` clusters (CTAs), as many
+// as run at the same time, and the launch.
+template <int MODE, typename... KArgs, typename... Args>
+cudaError_t launch_teams(void (*kern)(KArgs...), int split, int threads, int smem, int64_t& clusters, int registers,
+                         std::atomic<uint64_t> (&cache)[kMaxDevices], cudaStream_t s, Args... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int64_t parts = std::min(norm_most_parts(p, a.M), (a.M + teams - 1) / teams);
   if constexpr (MODE == kClusterTeam) {
-    static std::atomic<uint64_t> clusters[kMaxDevices] = {};
-    if (parts > sm_count() / 2 / p.split) parts = std::min(parts, active_clusters(kern, cfg, p.split, clusters));
+    if (clusters > sm_count() / 2 / split) clusters = std::min(clusters, active_clusters(kern, cfg, split, cache));
     cfg.numAttrs = 2;
   } else {
-    const int by_regs = 65536 / ((kernel_registers(kern, regs) + 7) / 8 * 8 * threads);
+    const int by_regs = 65536 / ((registers + 7) / 8 * 8 * threads);
     const int by_smem = kSmemPerSm / (smem + 4096);
-    parts = std::min(parts, static_cast<int64_t>(sm_count()) * std::max(1, std::min(by_regs, by_smem)));
+    clusters = std::min(clusters, static_cast<int64_t>(sm_count()) * std::max(1, std::min(by_regs, by_smem)));
     cfg.attrs = attr + 1;
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(parts * p.split));
-  e = cudaLaunchKernelEx(&cfg, kern, a, p.team, p.split, p.cols);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename T, bool COPY, int MODE, int C>
+cudaError_t launch_layernorm_t(const NormFwd& a, const NormPlan& p, cudaStream_t s) {
+  static std::atomic<bool> done[kMaxDevices] = {};
+  static std::atomic<int> regs[kMaxDevices] = {};
+  static std::atomic<uint64_t> active[kMaxDevices] = {};
+  auto kern = layernorm_kernel<T, COPY, MODE, C>;
+  const int most = MODE == kWarpTeam ? kNormFwdMaxTeams : 15;  // named barriers
+  const int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(most, kNormFwdThreads / p.team));
+  const int smem = teams * 4 * p.team * C * 16;
+  const cudaError_t e = set_smem(kern, kNormSmemMax, done);
+  if (e != cudaSuccess) return e;
+  int64_t parts = (a.M + teams - 1) / teams;
+  return launch_teams<MODE>(kern, p.split, teams * p.team, smem, parts, kernel_registers(kern, regs), active, s, a,
+                            p.team, p.split, p.cols);
+}
+
+template <typename T, bool COPY>
+cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
+  constexpr int V = Piece<T>::V;
+  const NormPlan p = norm_plan(a.K);
+  if (p.split > 1) return launch_layernorm_t<T, COPY, kClusterTeam, 16 / V>(a, p, s);
+  if (p.cv == 16) return launch_layernorm_t<T, COPY, kCtaTeam, 16 / V>(a, p, s);
+  if (p.team == 32) return launch_layernorm_t<T, COPY, kWarpTeam, 8 / V>(a, p, s);
+  return launch_layernorm_t<T, COPY, kCtaTeam, 8 / V>(a, p, s);
+}
+
+template <typename T, bool COPY, bool RMS, int MODE, int C, int R>
+cudaError_t launch_norm_bwd(const NormBwd& a, const NormPlan& p, cudaStream_t s) {
+  static std::atomic<bool> done[kMaxDevices] = {};
+  static std::atomic<int> regs[kMaxDevices] = {};
+  static std::atomic<uint64_t> active[kMaxDevices] = {};
+  auto kern = norm_bwd_kernel<T, COPY, RMS, MODE, C, R>;
+  int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(kNormMaxTeams, kNormBwdThreads / p.team));
+  while (teams > 1 && norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols) > kNormSmemMax) --teams;
+  const int threads = teams * p.team;
+  const int smem = norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols);
+  cudaError_t e = set_smem(kern, kNormSmemMax, done);
+  if (e != cudaSuccess) return e;
+  int64_t parts = std::min(norm_most_parts(p, a.M), (a.M + teams - 1) / teams);
+  e = launch_teams<MODE>(kern, p.split, threads, smem, parts, kernel_registers(kern, regs), active, s, a, p.team,
+                         p.split, p.cols);
   if (e != cudaSuccess || parts == 1 || (a.dgain == nullptr && a.dbias == nullptr)) return e;
   return launch_pdl(norm_join_kernel, dim3(static_cast<unsigned>(a.K / (4 * kNormJoinLanes)), a.dbias != nullptr ? 2 : 1),
                     dim3(kNormJoinThreads), 0, s, static_cast<const float*>(a.part), static_cast<int>(parts), a.K,
@@ -197,10 +223,11 @@ bitnet_status bitnet_layernorm(const void* x, int dtype, int64_t M, int64_t K, c
     return BITNET_ERR_INVALID_ARG;
   if (!valid_rows(M, K)) return BITNET_ERR_UNSUPPORTED_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int k = static_cast<int>(K);
-  return from_cuda(dtype == BITNET_BF16
-                       ? launch_layernorm<__nv_bfloat16>(x, M, k, gain, bias, eps, y, mean, rstd, x8, x_scale, s)
-                       : launch_layernorm<float>(x, M, k, gain, bias, eps, y, mean, rstd, x8, x_scale, s));
+  const NormFwd a = {x, gain, bias, y, mean, rstd, x8, x_scale, eps, M, static_cast<int>(K)};
+  if (dtype == BITNET_BF16)
+    return from_cuda(x8 != nullptr ? launch_layernorm<__nv_bfloat16, true>(a, s)
+                                   : launch_layernorm<__nv_bfloat16, false>(a, s));
+  return from_cuda(x8 != nullptr ? launch_layernorm<float, true>(a, s) : launch_layernorm<float, false>(a, s));
 }
 
 size_t bitnet_norm_backward_workspace_bytes(int64_t M, int64_t K) {

@@ -27,63 +27,9 @@
 #pragma once
 
 #include "norm.cuh"
+#include "pieces.cuh"
 
 namespace bitnet {
-
-// ------------------------------------------------- pairs of fp32 values
-
-BN_DEV uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-BN_DEV float f2_lo(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
-BN_DEV float f2_hi(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
-BN_DEV uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-BN_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-BN_DEV uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-// --------------------------------------------------------- 16-byte pieces
-
-// A piece is 16 bytes of T: V values, as V/2 pairs.
-template <typename T>
-struct Piece {
-  static constexpr int V = 16 / static_cast<int>(sizeof(T));
-  uint64_t p[V / 2];
-};
-
-BN_DEV void unpack_piece(const uint4& u, Piece<__nv_bfloat16>& r) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.p[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-}
-
-BN_DEV void unpack_piece(const uint4& u, Piece<float>& r) {
-  r.p[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
-  r.p[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
-}
-
-BN_DEV uint4 pack_piece(const Piece<__nv_bfloat16>& r) {
-  return make_uint4(pack_bf16x2(f2_lo(r.p[0]), f2_hi(r.p[0])), pack_bf16x2(f2_lo(r.p[1]), f2_hi(r.p[1])),
-                    pack_bf16x2(f2_lo(r.p[2]), f2_hi(r.p[2])), pack_bf16x2(f2_lo(r.p[3]), f2_hi(r.p[3])));
-}
-
-BN_DEV uint4 pack_piece(const Piece<float>& r) {
-  return make_uint4(__float_as_uint(f2_lo(r.p[0])), __float_as_uint(f2_hi(r.p[0])), __float_as_uint(f2_lo(r.p[1])),
-                    __float_as_uint(f2_hi(r.p[1])));
-}
 
 // Four codes of an 8-bit copy (act8_decode's arithmetic) as two pairs.
 BN_DEV void decode_codes4(uint32_t codes, uint64_t scale2, uint64_t* p) {
@@ -97,74 +43,10 @@ BN_DEV void decode_codes4(uint32_t codes, uint64_t scale2, uint64_t* p) {
   }
 }
 
-// ------------------------------------------------------ shared memory
-
-// Volatile: a second read is a second load, not a register kept since the first.
-BN_DEV uint4 lds128_again(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-BN_DEV uint2 lds64_again(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-BN_DEV uint32_t lds32_again(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-// Four values to shared memory of a CTA of the cluster, counted as 16 bytes by
-// an mbarrier there.
-BN_DEV void send_cluster(uint32_t cluster_addr, const float* v, uint32_t cluster_bar) {
-  asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(cluster_bar)
-      : "memory");
-}
-// Barrier of one team of a CTA.
-BN_DEV void team_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
-
-// ------------------------------------------------------------ reductions
-
-// Sums of N (4 or 8) values over the warp: value i ends up in the 32 / N lanes
-// from lane i * 32 / N on.
-BN_DEV float warp_sums(const float (&v)[4], int lane) {
-  const bool h16 = lane & 16, h8 = lane & 8;
-  const float a = (h16 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, h16 ? v[0] : v[2], 16);
-  const float b = (h16 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, h16 ? v[1] : v[3], 16);
-  float k = (h8 ? b : a) + __shfl_xor_sync(0xffffffffu, h8 ? a : b, 8);
-#pragma unroll
-  for (int d = 4; d >= 1; d >>= 1) k += __shfl_xor_sync(0xffffffffu, k, d);
-  return k;
-}
-BN_DEV float warp_sums(const float (&v)[8], int lane) {
-  float a[4], b[2];
-  const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    a[i] = (h16 ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, h16 ? v[i] : v[i + 4], 16);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    b[i] = (h8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, h8 ? a[i] : a[i + 2], 8);
-  float k = (h4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, h4 ? b[0] : b[1], 4);
-  k += __shfl_xor_sync(0xffffffffu, k, 2);
-  return k + __shfl_xor_sync(0xffffffffu, k, 1);
-}
-
 // ---------------------------------------------------------------- kernel
 
 constexpr int kNormBwdThreads = 512;  // at most
 constexpr int kNormMaxTeams = 8;      // of a CTA
-constexpr int kNormMaxWarpSums = 64;  // warps of a team over its cluster
-
-enum NormTeam { kWarpTeam, kCtaTeam, kClusterTeam };
-
 // Bytes of a row in the ring: dy, then x or its codes, each for all of the
 // team's threads (what lies past the row's columns stays zero).
 template <typename T, bool COPY, int C>
@@ -264,10 +146,7 @@ __global__ void __launch_bounds__(kNormBwdThreads)
   Piece<T> gain[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    const uint32_t one = sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u;
-    unpack_piece(a.gain != nullptr && ok[j] ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.gain) + col0 +
-                                                                                   (t + j * team) * V))
-                                            : make_uint4(one, one, one, one),
+    unpack_piece(piece_or(static_cast<const T*>(a.gain) + col0 + (t + j * team) * V, a.gain != nullptr && ok[j], 1.0f),
                  gain[j]);
   }
 

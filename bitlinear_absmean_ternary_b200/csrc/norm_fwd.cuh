@@ -1,0 +1,365 @@
+// Layer norm (formulas in norm.cuh), with the 8-bit copy of x for the backward
+// pass written on the way when it is wanted.
+//
+// Built like the backward kernel (norm_bwd.cuh): a team of threads (a warp,
+// part of a CTA, a CTA or a cluster of CTAs) walks the rows u, u + U, ...; rows
+// stream into shared memory by bulk copies, a batch of two rows ahead of the
+// batch at work; each thread takes its C pieces of 16 bytes into registers
+// once, and keeps its columns' gain and bias there for all rows.
+//
+// One stage of sums.  A warp sums x - p and (x - p)^2, p the mean of its first
+// piece, and makes of them its sum S_w and the squares about its own mean
+//
+//   Q_w = sum (x - p)^2 - (sum (x - p))^2 / n_w.
+//
+// The n_p values behind p alone have squares n_p (p - mean_w)^2 about mean_w, so
+// the first term is at most 1 + n_w / n_p times Q_w and little cancels, whatever
+// the row's mean (with a mean of 1000 deviations, or an outlier in the piece
+// itself).  The team joins the warps' the same way about the first warp's mean:
+//
+//   d_w = S_w / n_w - S_0 / n_0,  mean = S_0 / n_0 + sum n_w d_w / K
+//   K var = sum (Q_w + n_w d_w^2) - (sum n_w d_w)^2 / K
+//
+// In a cluster the warps' sums travel by st.async, as in the backward kernel.
+//
+// Other forms measured for M = 2048, K = 21504 (M = 4096, K = 2560): a CTA per
+// row that reads it three times from L1 or L2 41 us (16.2); a row in the
+// registers of up to 896 threads 60 (19), of few threads with 80 columns each
+// 77 (14.4); this one XX (YY).
+#pragma once
+
+#include "norm.cuh"
+#include "pieces.cuh"
+
+namespace bitnet {
+
+struct NormFwd {
+  const void* x;
+  const void* gain;  // or null
+  const void* bias;  // or null
+  void* y;
+  float* mean;       // or null
+  float* rstd;       // or null
+  int8_t* x8;        // or null
+  float* x_scale;
+  float eps;
+  int64_t M;
+  int K;
+};
+
+constexpr int kNormFwdThreads = 512;  // at most
+constexpr int kNormFwdMaxTeams = 16;  // of a CTA
+
+// Largest magnitude of a piece as a bit pattern (they order like the values).
+BN_DEV uint32_t piece_top(const uint4& u, __nv_bfloat16) {
+  const uint32_t m = max_u16x2(max_u16x2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                               max_u16x2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+  return max(m << 16, m & 0xFFFF0000u);
+}
+BN_DEV uint32_t piece_top(const uint4& u, float) {
+  return max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu));
+}
+
+// The 8-bit copies of N pieces of every lane (act8_encode's arithmetic): the
+// lanes of a group (64 / V neighbours) share out the divisions, one piece's
+// each.  Every lane of the warp takes part; what is not present is not stored.
+template <typename T, int N>
+BN_DEV void store_act8_pieces(const uint4 (&raw)[N], const int64_t (&at)[N], const bool (&present)[N], int8_t* x8,
+                              float* x_scale, int lane) {
+  constexpr int V = Piece<T>::V, L = kAct8Group / V;  // lanes of a group
+  static_assert(N <= L, "a lane for each piece");
+  uint32_t top = 0;
+  int64_t my_at = 0;
+  bool my_present = false;
+  const int who = lane & (L - 1);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t m = piece_top(raw[i], T());
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (who == i) {
+      top = m;
+      my_at = at[i];
+      my_present = present[i];
+    }
+  }
+  const bool live = top >= kAct8TinyBits && top < kInfBits;
+  const float amax = live ? __uint_as_float(top) : 1.0f;
+  const float inv = live ? __fdiv_rn(127.0f, amax) : 0.0f;
+  const float scale = fminf(__fdiv_rn(amax, 127.0f), __uint_as_float(kAct8MaxScaleBits));
+  if (my_present)
+    x_scale[my_at / kAct8Group] = live ? scale : top < kAct8TinyBits ? 0.0f : __uint_as_float(0x7FC00000u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float k = __shfl_sync(0xffffffffu, inv, (lane & ~(L - 1)) | i);
+    Piece<T> x;
+    unpack_piece(raw[i], x);
+    uint32_t w[V / 4];
+    // scalar steps: a packed product and a packed sum become one fma, which
+    // rounds once where the definition rounds twice (x = amax / 2 then differs)
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      w[j] = pack4_s8(f32_to_s8_rne_bits(__fmul_rn(f2_lo(x.p[2 * j]), k)),
+                      f32_to_s8_rne_bits(__fmul_rn(f2_hi(x.p[2 * j]), k)),
+                      f32_to_s8_rne_bits(__fmul_rn(f2_lo(x.p[2 * j + 1]), k)),
+                      f32_to_s8_rne_bits(__fmul_rn(f2_hi(x.p[2 * j + 1]), k)));
+      if (k == 0.0f) w[j] = 0;  // zeros, or a group with an Inf or a NaN
+    }
+    if (present[i]) {
+      if constexpr (V == 8) *reinterpret_cast<uint2*>(x8 + at[i]) = make_uint2(w[0], w[V / 4 - 1]);
+      else *reinterpret_cast<uint32_t*>(x8 + at[i]) = w[0];
+    }
+  }
+}
+
+// team: threads per row and CTA (a multiple of 32; blockDim.x is a multiple of
+// it; 32 for kWarpTeam).  split: CTAs per row, the cluster size (1 but for
+// kClusterTeam).  cols: columns per CTA, a multiple of 64 (the last of a
+// cluster may have fewer).
+template <typename T, bool COPY, int MODE, int C>
+__global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFwd a, int team, int split, int cols) {
+  constexpr int V = Piece<T>::V, R = 2;
+  constexpr int kEntries = MODE == kClusterTeam ? kNormMaxWarpSums : 16;
+  constexpr int kPerLane = MODE == kClusterTeam ? 2 : 1;  // entries a lane joins
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float4 red[2][kEntries];  // of each warp: S_w and Q_w of both rows
+  __shared__ __align__(8) uint64_t full[kNormFwdMaxTeams][2];
+  __shared__ __align__(8) uint64_t sent[2];
+
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  const int my_team = MODE == kClusterTeam ? 0 : tid / team, t = tid - my_team * team;
+  const int nteams = MODE == kClusterTeam ? 1 : static_cast<int>(blockDim.x) / team, tw = team >> 5, warp = t >> 5;
+  const int rank = MODE == kClusterTeam ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cluster_id = static_cast<int>(MODE == kClusterTeam ? blockIdx.x / static_cast<unsigned>(split) : blockIdx.x);
+  const int clusters = static_cast<int>(MODE == kClusterTeam ? gridDim.x / static_cast<unsigned>(split) : gridDim.x);
+  const int U = clusters * nteams;
+  const int unit = cluster_id * nteams + my_team;
+  const int M = static_cast<int>(a.M);
+  const int rows = unit < M ? (M - 1 - unit) / U + 1 : 0;
+  const int col0 = rank * cols;
+  const int my_cols = a.K - col0 < cols ? a.K - col0 : cols;
+
+  // The ring of this team: two stages of R rows.
+  const int row_bytes = team * C * 16;
+  uint8_t* ring = smem + my_team * 2 * R * row_bytes;
+  uint64_t* my_full = full[my_team];
+  if (tid == 0) {
+    for (int i = 0; i < nteams; ++i) {
+      mbar_init(&full[i][0], 1);
+      mbar_init(&full[i][1], 1);
+    }
+    mbar_init(&sent[0], 1);
+    mbar_init(&sent[1], 1);
+    fence_barrier_init();
+  }
+  bool ok[C];  // piece t + j team exists; no copy writes the others' places
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    ok[j] = (t + j * team) * V < my_cols;
+    if (!ok[j])
+      for (int r = 0; r < 2 * R; ++r)
+        *reinterpret_cast<uint4*>(ring + r * row_bytes + 16 * (t + j * team)) = make_uint4(0, 0, 0, 0);
+  }
+  // columns of warp w of CTA `of`, 0 where there is no such warp
+  auto columns = [&](int of, int w) {
+    const int mine = min(cols, a.K - of * cols);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) n += max(0, min(32 * V, mine - (w * 32 + j * team) * V));
+    return static_cast<float>(n);
+  };
+  const float n_mine = columns(rank, warp), inv_mine = n_mine > 0.0f ? 1.0f / n_mine : 0.0f;
+  const float inv_first = 1.0f / columns(0, 0);
+  float n_of[kPerLane], inv_of[kPerLane];  // of entries lane, lane + 32
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int e = lane + 32 * i;
+    n_of[i] = e < split * tw ? columns(e / tw, e % tw) : 0.0f;
+    inv_of[i] = n_of[i] > 0.0f ? 1.0f / n_of[i] : 0.0f;
+  }
+  if constexpr (MODE == kClusterTeam) cluster_sync();
+  else __syncthreads();
+  pdl_wait();
+  // Clusters of the next grid that start while this one's still run take their
+  // places and stretch its tail: 46.6 us against 40.8 for M = 2048, K = 21504.
+  if constexpr (MODE != kClusterTeam) pdl_launch_dependents();
+
+  const uint64_t once = policy_evict_first();
+  const int64_t step = static_cast<int64_t>(U) * a.K;
+  const int64_t first = static_cast<int64_t>(unit) * a.K + col0;
+  auto fill = [&](int row, int stage) {  // one thread of the team: rows row .. row + R - 1
+    const int n = rows - row < R ? rows - row : R;
+    const uint32_t bytes = static_cast<uint32_t>(my_cols * static_cast<int>(sizeof(T)));
+    mbar_arrive_expect_tx(&my_full[stage], static_cast<uint32_t>(n) * bytes);
+#pragma unroll 1
+    for (int r = 0; r < n; ++r)
+      bulk_copy_g2s(ring + (stage * R + r) * row_bytes,
+                    static_cast<const T*>(a.x) + first + static_cast<int64_t>(row + r) * step, bytes, &my_full[stage],
+                    once);
+  };
+  if (t == 0) {
+    if (rows > 0) fill(0, 0);
+    if (rows > R) fill(R, 1);
+  }
+  uint4 g[C], h[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int c = col0 + (t + j * team) * V;
+    g[j] = piece_or(static_cast<const T*>(a.gain) + c, a.gain != nullptr && ok[j], 1.0f);
+    h[j] = piece_or(static_cast<const T*>(a.bias) + c, a.bias != nullptr && ok[j], 0.0f);
+  }
+
+  const float inv_k = 1.0f / static_cast<float>(a.K);
+  const uint32_t mine = smem_addr(ring) + 16 * t, pivot_at = smem_addr(ring) + 16 * 32 * warp;
+  int64_t at = first + t * V;  // of this thread's first piece in the row at work
+  int dead = -1;               // the batch at which a wait gave up: no more waits or fills, the results are lost
+  int b = 0;
+  for (int row = 0; row < rows; row += R, ++b) {
+    const int stage = b & 1;
+    const uint32_t parity = static_cast<uint32_t>(b >> 1) & 1u;
+    if (dead < 0 && !mbar_wait(&my_full[stage], parity)) dead = b;
+    uint4 raw[R][C];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < C; ++j) raw[r][j] = lds128_again(mine + (stage * R + r) * row_bytes + 16 * j * team);
+
+    // the warp's sums about its pivots: value i of {S, Q of row 0, S, Q of row 1}
+    // ends up in lanes 8 i .. 8 i + 7
+    float sums[4], pivot[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      Piece<T> x;
+      unpack_piece(lds128_again(pivot_at + (stage * R + r) * row_bytes), x);
+      uint64_t s0 = x.p[0];
+#pragma unroll
+      for (int i = 1; i < V / 2; ++i) s0 = f2_add(s0, x.p[i]);
+      pivot[r] = (f2_lo(s0) + f2_hi(s0)) * (1.0f / V);
+      const uint64_t p2 = f2(-pivot[r], -pivot[r]);
+      s0 = 0;
+      uint64_t s1 = 0;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        unpack_piece(raw[r][j], x);
+        uint64_t t0 = 0, t1 = 0;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const uint64_t d = f2_add(x.p[i], p2);
+          t0 = f2_add(t0, d);
+          t1 = f2_fma(d, d, t1);
+        }
+        if (ok[j]) {
+          s0 = f2_add(s0, t0);
+          s1 = f2_add(s1, t1);
+        }
+      }
+      sums[2 * r] = f2_lo(s0) + f2_hi(s0);
+      sums[2 * r + 1] = f2_lo(s1) + f2_hi(s1);
+    }
+    float k = warp_sums(sums, lane);
+    const float other = __shfl_xor_sync(0xffffffffu, k, 8);  // the S of a Q's lanes
+    k = lane & 8 ? k - other * other * inv_mine : k + n_mine * (lane & 16 ? pivot[1] : pivot[0]);
+
+    float mean[R], var[R];
+    if constexpr (MODE == kWarpTeam) {
+      __syncwarp();
+      k *= inv_k;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        mean[r] = __shfl_sync(0xffffffffu, k, 16 * r);
+        var[r] = __shfl_sync(0xffffffffu, k, 16 * r + 8);
+      }
+    } else {
+      float4* buf = &red[stage][my_team * tw];
+      if constexpr (MODE == kCtaTeam) {
+        if ((lane & 7) == 0) reinterpret_cast<float*>(buf + warp)[lane >> 3] = k;
+        team_sync(1 + my_team, team);
+      } else {
+        if (tid == 0) mbar_arrive_expect_tx(&sent[stage], static_cast<uint32_t>(split * tw * 16));
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, k, 8 * i);
+        if (lane < split)
+          send_cluster(mapa_shared(smem_addr(buf + rank * tw + warp), lane), v, mapa_shared(smem_addr(&sent[stage]), lane));
+        if (dead < 0 && !mbar_wait_cluster(&sent[stage], parity)) dead = b;
+      }
+      const float4 e0 = buf[0];
+      const float m0 = e0.x * inv_first, m1 = e0.z * inv_first;
+      sums[0] = sums[1] = sums[2] = sums[3] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) {
+        if (n_of[i] > 0.0f) {
+          const float4 e = buf[lane + 32 * i];
+          const float d0 = e.x * inv_of[i] - m0, d1 = e.z * inv_of[i] - m1;
+          sums[0] += n_of[i] * d0;
+          sums[1] += e.y + n_of[i] * d0 * d0;
+          sums[2] += n_of[i] * d1;
+          sums[3] += e.w + n_of[i] * d1 * d1;
+        }
+      }
+      k = warp_sums(sums, lane);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float d = __shfl_sync(0xffffffffu, k, 16 * r) * inv_k;
+        mean[r] = (r == 0 ? m0 : m1) + d;
+        var[r] = __shfl_sync(0xffffffffu, k, 16 * r + 8) * inv_k - d * d;
+      }
+    }
+    // every thread of the team has its values of the stage in registers
+    if (t == 0 && row + 2 * R < rows && dead < 0) {
+      fence_proxy_async_smem();
+      fill(row + 2 * R, stage);
+    }
+
+    float rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) rstd[r] = __fdiv_rn(1.0f, __fsqrt_rn(fmaxf(var[r], 0.0f) + a.eps));
+    const bool two = row + 1 < rows;
+    if (t == 0 && rank == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int64_t m = unit + static_cast<int64_t>(row + r) * U;
+        if (a.mean != nullptr && (r == 0 || two)) a.mean[m] = mean[r];
+        if (a.rstd != nullptr && (r == 0 || two)) a.rstd[m] = rstd[r];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      Piece<T> gg, hh;
+      unpack_piece(g[j], gg);
+      unpack_piece(h[j], hh);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint64_t m2 = f2(-mean[r], -mean[r]), r2 = f2(rstd[r], rstd[r]);
+        Piece<T> x, o;
+        unpack_piece(raw[r][j], x);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) o.p[i] = f2_fma(f2_mul(f2_add(x.p[i], m2), r2), gg.p[i], hh.p[i]);
+        if (ok[j] && (r == 0 || two))
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + at + r * step + j * team * V) = pack_piece(o);
+      }
+    }
+    if constexpr (COPY) {
+      uint4 p[R * C];
+      int64_t p_at[R * C];
+      bool present[R * C];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          p[r * C + j] = raw[r][j];
+          p_at[r * C + j] = at + r * step + j * team * V;
+          present[r * C + j] = ok[j] && (r == 0 || two);
+        }
+      store_act8_pieces<T>(p, p_at, present, a.x8, a.x_scale, lane);
+    }
+    at += R * step;
+  }
+  // After a timeout: the copies still in flight land before shared memory goes away.
+  if (dead >= 0 && t == 0)
+    for (int i = dead; i < dead + 2 && i * R < rows; ++i) mbar_wait(&my_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u);
+  if constexpr (MODE == kClusterTeam) cluster_sync();  // nothing more is sent to a CTA that has ended
+  pdl_launch_dependents();
+}
+
+}  // namespace bitnet
