@@ -7,8 +7,9 @@
 //
 // as the gated product's epilogue computes h.  The forward kernel can leave u
 // and g in 8 bits (act8.cuh) in the same pass; the backward kernel reads them
-// from there, or as they were.  Elementwise, bound by memory: a thread per 8
-// values.
+// from there, or as they were.  Elementwise, bound by memory: 0.95 to 1.02 of
+// measured HBM at M = 4096, F = 6912 bf16.  A thread has one 16-byte piece of
+// every array in flight, U of them in the forward kernel that writes copies.
 #pragma once
 
 #include "act8.cuh"
@@ -17,61 +18,80 @@ namespace bitnet {
 
 constexpr int kGateThreads = 256;
 
-template <typename T, bool COPY>
+template <typename T>
+BN_DEV void relu_piece(const Piece<T>& g, Piece<T>& r) {
+#pragma unroll
+  for (int i = 0; i < Piece<T>::V / 2; ++i) {
+    const float lo = f2_lo(g.p[i]), hi = f2_hi(g.p[i]);
+    r.p[i] = f2(lo > 0.0f ? lo : 0.0f, hi > 0.0f ? hi : 0.0f);
+  }
+}
+
+template <typename T, bool COPY, int U>
 __global__ void __launch_bounds__(kGateThreads)
-    relu2_gate_kernel(const T* __restrict__ u, const T* __restrict__ g, int64_t chunks, T* __restrict__ h,
+    relu2_gate_kernel(const T* __restrict__ u, const T* __restrict__ g, int64_t pieces, T* __restrict__ h,
                       int8_t* __restrict__ u8, float* __restrict__ u_scale, int8_t* __restrict__ g8,
                       float* __restrict__ g_scale) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kGateThreads + threadIdx.x;
+  constexpr int V = Piece<T>::V;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGateThreads * U) + threadIdx.x;
+  uint4 ru[U], rg[U];
+  int64_t at[U];
+  bool present[U];
   pdl_wait();
-  F8 fu = {}, fg = {};
-  if (c < chunks) {
-    fu = load8(u + 8 * c);
-    fg = load8(g + 8 * c);
-    F8 fh;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float r = fg.v[e] > 0.0f ? fg.v[e] : 0.0f;
-      fh.v[e] = __fmul_rn(__fmul_rn(r, r), fu.v[e]);
-    }
-    store8(h + 8 * c, fh);
+  for (int i = 0; i < U; ++i) {
+    const int64_t p = first + i * kGateThreads;
+    present[i] = p < pieces;
+    at[i] = p * V;
+    ru[i] = present[i] ? ldg_once(u + at[i]) : make_uint4(0, 0, 0, 0);
+    rg[i] = present[i] ? ldg_once(g + at[i]) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    Piece<T> fu, fg, r, o;
+    unpack_piece(ru[i], fu);
+    unpack_piece(rg[i], fg);
+    relu_piece(fg, r);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) o.p[j] = f2_mul(f2_mul(r.p[j], r.p[j]), fu.p[j]);
+    if (present[i]) *reinterpret_cast<uint4*>(h + at[i]) = pack_piece(o);
   }
   if constexpr (COPY) {
-    float su, sg;
-    const uint2 qu = act8_encode(fu, su), qg = act8_encode(fg, sg);
-    if (c < chunks) {
-      reinterpret_cast<uint2*>(u8)[c] = qu;
-      reinterpret_cast<uint2*>(g8)[c] = qg;
-      if ((c & 7) == 0) {
-        u_scale[c >> 3] = su;
-        g_scale[c >> 3] = sg;
-      }
-    }
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    store_act8_pieces<T>(ru, at, present, u8, u_scale, lane);
+    store_act8_pieces<T>(rg, at, present, g8, g_scale, lane);
   }
   pdl_launch_dependents();
 }
 
 template <typename T, bool COPY>
 __global__ void __launch_bounds__(kGateThreads)
-    relu2_gate_backward_kernel(const T* __restrict__ dh, int64_t chunks, const T* __restrict__ u,
+    relu2_gate_backward_kernel(const T* __restrict__ dh, int64_t pieces, const T* __restrict__ u,
                                const T* __restrict__ g, const int8_t* __restrict__ u8,
                                const float* __restrict__ u_scale, const int8_t* __restrict__ g8,
                                const float* __restrict__ g_scale, T* __restrict__ du, T* __restrict__ dg) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kGateThreads + threadIdx.x;
+  constexpr int V = Piece<T>::V;
+  const int64_t p = static_cast<int64_t>(blockIdx.x) * kGateThreads + threadIdx.x;
   pdl_wait();
-  if (c < chunks) {
-    const F8 d = load8(dh + 8 * c);
-    const F8 fu = COPY ? load_act8(u8, u_scale, c) : load8(u + 8 * c);
-    const F8 fg = COPY ? load_act8(g8, g_scale, c) : load8(g + 8 * c);
-    F8 a, b;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float r = fg.v[e] > 0.0f ? fg.v[e] : 0.0f;
-      a.v[e] = d.v[e] * (r * r);
-      b.v[e] = d.v[e] * fu.v[e] * (2.0f * r);
+  if (p < pieces) {
+    Piece<T> d, fu, fg, r, a, b;
+    unpack_piece(ldg_once(dh + p * V), d);
+    if constexpr (COPY) {
+      const uint2 cu = load_codes(u8 + p * V, T()), cg = load_codes(g8 + p * V, T());
+      decode_piece(cu, __ldg(u_scale + p * V / kAct8Group), fu);
+      decode_piece(cg, __ldg(g_scale + p * V / kAct8Group), fg);
+    } else {
+      unpack_piece(ldg_once(u + p * V), fu);
+      unpack_piece(ldg_once(g + p * V), fg);
     }
-    store8(du + 8 * c, a);
-    store8(dg + 8 * c, b);
+    relu_piece(fg, r);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      a.p[j] = f2_mul(d.p[j], f2_mul(r.p[j], r.p[j]));
+      b.p[j] = f2_mul(f2_mul(d.p[j], fu.p[j]), f2_add(r.p[j], r.p[j]));
+    }
+    *reinterpret_cast<uint4*>(du + p * V) = pack_piece(a);
+    *reinterpret_cast<uint4*>(dg + p * V) = pack_piece(b);
   }
   pdl_launch_dependents();
 }

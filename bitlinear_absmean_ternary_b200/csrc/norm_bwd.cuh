@@ -27,21 +27,8 @@
 #pragma once
 
 #include "norm.cuh"
-#include "pieces.cuh"
 
 namespace bitnet {
-
-// Four codes of an 8-bit copy (act8_decode's arithmetic) as two pairs.
-BN_DEV void decode_codes4(uint32_t codes, uint64_t scale2, uint64_t* p) {
-  const uint32_t w = codes ^ 0x80808080u;
-  const uint64_t bias = f2(-8388736.0f, -8388736.0f);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t v = f2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i))),
-                          __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i + 1))));
-    p[i] = f2_mul(f2_add(v, bias), scale2);
-  }
-}
 
 // ---------------------------------------------------------------- kernel
 
@@ -213,7 +200,7 @@ __global__ void __launch_bounds__(kNormBwdThreads)
         for (int j = 0; j < C; ++j) scale[r][j] = scale_n[r][j];
     }
     fetch_small(row + R);
-    if (dead < 0 && !mbar_wait(&my_full[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
+    if (dead < 0 && !mbar_wait_idle(&my_full[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
     const int base = (b & 1) * R * row_bytes;
 
     float sums[NV];
@@ -269,7 +256,7 @@ __global__ void __launch_bounds__(kNormBwdThreads)
 #pragma unroll
           for (int i = 0; i < NV; i += 4) send_cluster(to + 4 * i, mine + i, bar);
         }
-        if (dead < 0 && !mbar_wait_cluster(&sent[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
+        if (dead < 0 && !mbar_wait_idle(&sent[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
       }
       k = 0.0f;
 #pragma unroll 1
@@ -284,7 +271,7 @@ __global__ void __launch_bounds__(kNormBwdThreads)
     const float k1 = __shfl_xor_sync(0xffffffffu, k, kLanes);
     float row_r, row_a = 0.0f, row_b;
     if constexpr (RMS) {
-      row_r = __fdiv_rn(1.0f, __fsqrt_rn(k * inv_k + a.eps));
+      row_r = rsqrtf(k * inv_k + a.eps);
       row_b = -row_r * (row_r * k1 * inv_k);
     } else {
       row_r = rstd;

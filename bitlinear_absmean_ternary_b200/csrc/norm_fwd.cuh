@@ -29,7 +29,6 @@
 #pragma once
 
 #include "norm.cuh"
-#include "pieces.cuh"
 
 namespace bitnet {
 
@@ -49,68 +48,6 @@ struct NormFwd {
 
 constexpr int kNormFwdThreads = 512;  // at most
 constexpr int kNormFwdMaxTeams = 16;  // of a CTA
-
-// Largest magnitude of a piece as a bit pattern (they order like the values).
-BN_DEV uint32_t piece_top(const uint4& u, __nv_bfloat16) {
-  const uint32_t m = max_u16x2(max_u16x2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
-                               max_u16x2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
-  return max(m << 16, m & 0xFFFF0000u);
-}
-BN_DEV uint32_t piece_top(const uint4& u, float) {
-  return max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu));
-}
-
-// The 8-bit copies of N pieces of every lane (act8_encode's arithmetic): the
-// lanes of a group (64 / V neighbours) share out the divisions, one piece's
-// each.  Every lane of the warp takes part; what is not present is not stored.
-template <typename T, int N>
-BN_DEV void store_act8_pieces(const uint4 (&raw)[N], const int64_t (&at)[N], const bool (&present)[N], int8_t* x8,
-                              float* x_scale, int lane) {
-  constexpr int V = Piece<T>::V, L = kAct8Group / V;  // lanes of a group
-  static_assert(N <= L, "a lane for each piece");
-  uint32_t top = 0;
-  int64_t my_at = 0;
-  bool my_present = false;
-  const int who = lane & (L - 1);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint32_t m = piece_top(raw[i], T());
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (who == i) {
-      top = m;
-      my_at = at[i];
-      my_present = present[i];
-    }
-  }
-  const bool live = top >= kAct8TinyBits && top < kInfBits;
-  const float amax = live ? __uint_as_float(top) : 1.0f;
-  const float inv = live ? __fdiv_rn(127.0f, amax) : 0.0f;
-  const float scale = fminf(__fdiv_rn(amax, 127.0f), __uint_as_float(kAct8MaxScaleBits));
-  if (my_present)
-    x_scale[my_at / kAct8Group] = live ? scale : top < kAct8TinyBits ? 0.0f : __uint_as_float(0x7FC00000u);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float k = __shfl_sync(0xffffffffu, inv, (lane & ~(L - 1)) | i);
-    Piece<T> x;
-    unpack_piece(raw[i], x);
-    uint32_t w[V / 4];
-    // scalar steps: a packed product and a packed sum become one fma, which
-    // rounds once where the definition rounds twice (x = amax / 2 then differs)
-#pragma unroll
-    for (int j = 0; j < V / 4; ++j) {
-      w[j] = pack4_s8(f32_to_s8_rne_bits(__fmul_rn(f2_lo(x.p[2 * j]), k)),
-                      f32_to_s8_rne_bits(__fmul_rn(f2_hi(x.p[2 * j]), k)),
-                      f32_to_s8_rne_bits(__fmul_rn(f2_lo(x.p[2 * j + 1]), k)),
-                      f32_to_s8_rne_bits(__fmul_rn(f2_hi(x.p[2 * j + 1]), k)));
-      if (k == 0.0f) w[j] = 0;  // zeros, or a group with an Inf or a NaN
-    }
-    if (present[i]) {
-      if constexpr (V == 8) *reinterpret_cast<uint2*>(x8 + at[i]) = make_uint2(w[0], w[V / 4 - 1]);
-      else *reinterpret_cast<uint32_t*>(x8 + at[i]) = w[0];
-    }
-  }
-}
 
 // team: threads per row and CTA (a multiple of 32; blockDim.x is a multiple of
 // it; 32 for kWarpTeam).  split: CTAs per row, the cluster size (1 but for
@@ -217,7 +154,7 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
   for (int row = 0; row < rows; row += R, ++b) {
     const int stage = b & 1;
     const uint32_t parity = static_cast<uint32_t>(b >> 1) & 1u;
-    if (dead < 0 && !mbar_wait(&my_full[stage], parity)) dead = b;
+    if (dead < 0 && !mbar_wait_idle(&my_full[stage], parity)) dead = b;
     uint4 raw[R][C];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -281,7 +218,7 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
         for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, k, 8 * i);
         if (lane < split)
           send_cluster(mapa_shared(smem_addr(buf + rank * tw + warp), lane), v, mapa_shared(smem_addr(&sent[stage]), lane));
-        if (dead < 0 && !mbar_wait_cluster(&sent[stage], parity)) dead = b;
+        if (dead < 0 && !mbar_wait_idle(&sent[stage], parity)) dead = b;
       }
       const float4 e0 = buf[0];
       const float m0 = e0.x * inv_first, m1 = e0.z * inv_first;
@@ -313,7 +250,7 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
 
     float rstd[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) rstd[r] = __fdiv_rn(1.0f, __fsqrt_rn(fmaxf(var[r], 0.0f) + a.eps));
+    for (int r = 0; r < R; ++r) rstd[r] = rsqrtf(fmaxf(var[r], 0.0f) + a.eps);
     const bool two = row + 1 < rows;
     if (t == 0 && rank == 0) {
 #pragma unroll

@@ -2,7 +2,9 @@
 // row, and reductions over a warp and over the warps of a team.
 #pragma once
 
-#include "act8.cuh"
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
 
 namespace bitnet {
 
@@ -54,6 +56,11 @@ BN_DEV void unpack_piece(const uint4& u, Piece<float>& r) {
   r.p[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
 
+BN_DEV uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 BN_DEV uint4 pack_piece(const Piece<__nv_bfloat16>& r) {
   return make_uint4(pack_bf16x2(f2_lo(r.p[0]), f2_hi(r.p[0])), pack_bf16x2(f2_lo(r.p[1]), f2_hi(r.p[1])),
                     pack_bf16x2(f2_lo(r.p[2]), f2_hi(r.p[2])), pack_bf16x2(f2_lo(r.p[3]), f2_hi(r.p[3])));
@@ -62,6 +69,15 @@ BN_DEV uint4 pack_piece(const Piece<__nv_bfloat16>& r) {
 BN_DEV uint4 pack_piece(const Piece<float>& r) {
   return make_uint4(__float_as_uint(f2_lo(r.p[0])), __float_as_uint(f2_hi(r.p[0])), __float_as_uint(f2_lo(r.p[1])),
                     __float_as_uint(f2_hi(r.p[1])));
+}
+
+// 16 bytes of an array that is read once.
+BN_DEV uint4 ldg_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
 // A piece of a gain or bias at p, or V times `absent` where there is none: the
@@ -91,6 +107,29 @@ BN_DEV uint32_t lds32_again(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// mbar_wait and mbar_wait_cluster for many warps that wait together: a try
+// suspends its warp for up to 20 us, so waiting takes no issue slots from the
+// warps at work.
+BN_DEV bool mbar_wait_idle(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done != 0) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      flag_timeout();
+      return false;
+    }
+  }
 }
 
 // Barrier of one team of a CTA.
