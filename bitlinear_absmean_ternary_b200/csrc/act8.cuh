@@ -42,16 +42,16 @@ BN_DEV uint32_t piece_top(const uint4& u, float) {
   return max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu));
 }
 
-// The 8-bit copies of N pieces of every lane by the
-// formulas above: the lanes of a group (64 / V neighbours) share out the divisions, one piece's
-// each.  Every lane of the warp takes part; what is not present is not stored.
+// The 8-bit copies of N pieces of every lane, `stride` values apart from `at`
+// on, by the formulas above: the lanes of a group (64 / V neighbours) share out
+// the divisions, one piece's each.  Every lane of the warp takes part; what is
+// not present is not stored.
 template <typename T, int N>
-BN_DEV void store_act8_pieces(const uint4 (&raw)[N], const int64_t (&at)[N], const bool (&present)[N], int8_t* x8,
+BN_DEV void store_act8_pieces(const uint4 (&raw)[N], int64_t at, int stride, const bool (&present)[N], int8_t* x8,
                               float* x_scale, int lane) {
   constexpr int V = Piece<T>::V, L = kAct8Group / V;  // lanes of a group
   static_assert(N <= L, "a lane for each piece");
   uint32_t top = 0;
-  int64_t my_at = 0;
   bool my_present = false;
   const int who = lane & (L - 1);
 #pragma unroll
@@ -61,7 +61,6 @@ BN_DEV void store_act8_pieces(const uint4 (&raw)[N], const int64_t (&at)[N], con
     for (int d = 1; d < L; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (who == i) {
       top = m;
-      my_at = at[i];
       my_present = present[i];
     }
   }
@@ -70,7 +69,9 @@ BN_DEV void store_act8_pieces(const uint4 (&raw)[N], const int64_t (&at)[N], con
   const float inv = live ? __fdiv_rn(127.0f, amax) : 0.0f;
   const float scale = fminf(__fdiv_rn(amax, 127.0f), __uint_as_float(kAct8MaxScaleBits));
   if (my_present)
-    x_scale[my_at / kAct8Group] = live ? scale : top < kAct8TinyBits ? 0.0f : __uint_as_float(0x7FC00000u);
+    x_scale[(at + who * stride) / kAct8Group] = live ? scale
+                                                : top < kAct8TinyBits ? 0.0f : __uint_as_float(0x7FC00000u);
+  int8_t* to = x8 + at;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float k = __shfl_sync(0xffffffffu, inv, (lane & ~(L - 1)) | i);
@@ -88,8 +89,8 @@ BN_DEV void store_act8_pieces(const uint4 (&raw)[N], const int64_t (&at)[N], con
       if (k == 0.0f) w[j] = 0;  // zeros, or a group with an Inf or a NaN
     }
     if (present[i]) {
-      if constexpr (V == 8) *reinterpret_cast<uint2*>(x8 + at[i]) = make_uint2(w[0], w[V / 4 - 1]);
-      else *reinterpret_cast<uint32_t*>(x8 + at[i]) = w[0];
+      if constexpr (V == 8) *reinterpret_cast<uint2*>(to + i * stride) = make_uint2(w[0], w[V / 4 - 1]);
+      else *reinterpret_cast<uint32_t*>(to + i * stride) = w[0];
     }
   }
 }
@@ -128,17 +129,15 @@ __global__ void __launch_bounds__(kAct8Threads)
   constexpr int V = Piece<T>::V;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kAct8Threads * U) + threadIdx.x;
   uint4 raw[U];
-  int64_t at[U];
   bool present[U];
   pdl_wait();
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int64_t p = first + i * kAct8Threads;
     present[i] = p < pieces;
-    at[i] = p * V;
-    raw[i] = present[i] ? ldg_once(x + at[i]) : make_uint4(0, 0, 0, 0);
+    raw[i] = present[i] ? ldg_once(x + p * V) : make_uint4(0, 0, 0, 0);
   }
-  store_act8_pieces<T>(raw, at, present, x8, x_scale, static_cast<int>(threadIdx.x) & 31);
+  store_act8_pieces<T>(raw, first * V, kAct8Threads * V, present, x8, x_scale, static_cast<int>(threadIdx.x) & 31);
   pdl_launch_dependents();
 }
 

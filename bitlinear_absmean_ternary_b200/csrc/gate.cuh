@@ -35,16 +35,14 @@ __global__ void __launch_bounds__(kGateThreads)
   constexpr int V = Piece<T>::V;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGateThreads * U) + threadIdx.x;
   uint4 ru[U], rg[U];
-  int64_t at[U];
   bool present[U];
   pdl_wait();
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int64_t p = first + i * kGateThreads;
     present[i] = p < pieces;
-    at[i] = p * V;
-    ru[i] = present[i] ? ldg_once(u + at[i]) : make_uint4(0, 0, 0, 0);
-    rg[i] = present[i] ? ldg_once(g + at[i]) : make_uint4(0, 0, 0, 0);
+    ru[i] = present[i] ? ldg_once(u + p * V) : make_uint4(0, 0, 0, 0);
+    rg[i] = present[i] ? ldg_once(g + p * V) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -54,12 +52,12 @@ __global__ void __launch_bounds__(kGateThreads)
     relu_piece(fg, r);
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) o.p[j] = f2_mul(f2_mul(r.p[j], r.p[j]), fu.p[j]);
-    if (present[i]) *reinterpret_cast<uint4*>(h + at[i]) = pack_piece(o);
+    if (present[i]) *reinterpret_cast<uint4*>(h + (first + i * kGateThreads) * V) = pack_piece(o);
   }
   if constexpr (COPY) {
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    store_act8_pieces<T>(ru, at, present, u8, u_scale, lane);
-    store_act8_pieces<T>(rg, at, present, g8, g_scale, lane);
+    store_act8_pieces<T>(ru, first * V, kGateThreads * V, present, u8, u_scale, lane);
+    store_act8_pieces<T>(rg, first * V, kGateThreads * V, present, g8, g_scale, lane);
   }
   pdl_launch_dependents();
 }

@@ -26,6 +26,16 @@ constexpr int kNormClusterThreads = 256;
 // (M = 4096, K = 2560: 21.1 us with three CTAs per SM, 18.9 with three teams).
 constexpr int kNormCtasPerSm = 1;
 constexpr int kNormClusterCtasPerSm = 4;
+// Layer norm forward: a CTA per row of up to 16 KB, a cluster beyond, whose CTAs
+// take up to 16 KB of the row each, or 8 KB where bf16 rows leave an 8-bit copy
+// (M = 2048, K = 21504 with the copy 54.7 us against 60.9; without it 34.4
+// either way).  Up to four 16-byte pieces per thread (M = 4096, K = 6912: 26.2 us
+// with two, 23.1 with three, 20.8 with four, 24.4 with five), three with the
+// copy of bf16 rows, where four spill.
+constexpr int kNormFwdOneCtaBytes = 16384;
+constexpr int kNormFwdPieces = 4;
+constexpr int kNormFwdCopyPieces = 3;
+constexpr int kNormFwdTeamThreads = 512;  // several rows in a CTA up to this
 constexpr int kSmemPerSm = 233472;  // 228 KB
 constexpr int kNormSmemMax = 220 * 1024;
 
@@ -121,29 +131,60 @@ cudaError_t launch_teams(void (*kern)(KArgs...), int split, int threads, int sme
 }
 
 template <typename T, bool COPY, int MODE, int C>
-cudaError_t launch_layernorm_t(const NormFwd& a, const NormPlan& p, cudaStream_t s) {
+cudaError_t launch_layernorm_t(const NormFwd& a, int split, int cols, int team, cudaStream_t s) {
   static std::atomic<bool> done[kMaxDevices] = {};
   static std::atomic<int> regs[kMaxDevices] = {};
   static std::atomic<uint64_t> active[kMaxDevices] = {};
   auto kern = layernorm_kernel<T, COPY, MODE, C>;
+  const int team_smem = (4 + 2) * team * C * 16;  // two stages of two rows, gain and bias
   const int most = MODE == kWarpTeam ? kNormFwdMaxTeams : 15;  // named barriers
-  const int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(most, kNormFwdThreads / p.team));
-  const int smem = teams * 4 * p.team * C * 16;
+  const int teams = MODE == kClusterTeam
+                        ? 1
+                        : static_cast<int>(std::max<int64_t>(
+                              1, std::min<int64_t>({most, kNormFwdTeamThreads / team, kNormSmemMax / team_smem,
+                                                    (a.M + sm_count() - 1) / sm_count()})));
+  const int smem = teams * team_smem;
   const cudaError_t e = set_smem(kern, kNormSmemMax, done);
   if (e != cudaSuccess) return e;
   int64_t parts = (a.M + teams - 1) / teams;
-  return launch_teams<MODE>(kern, p.split, teams * p.team, smem, parts, kernel_registers(kern, regs), active, s, a,
-                            p.team, p.split, p.cols);
+  return launch_teams<MODE>(kern, split, teams * team, smem, parts, kernel_registers(kern, regs), active, s, a, team,
+                            split, cols);
+}
+
+// Pieces per thread: the most that leave at most an eighth of the team's
+// places empty.
+int pieces_per_thread(int pieces, int most) {
+  for (int c = most; c > 1; --c) {
+    const int places = (pieces + 32 * c - 1) / (32 * c) * 32 * c;
+    if (8 * (places - pieces) <= pieces) return c;
+  }
+  return 1;
 }
 
 template <typename T, bool COPY>
 cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
   constexpr int V = Piece<T>::V;
-  const NormPlan p = norm_plan(a.K);
-  if (p.split > 1) return launch_layernorm_t<T, COPY, kClusterTeam, 16 / V>(a, p, s);
-  if (p.cv == 16) return launch_layernorm_t<T, COPY, kCtaTeam, 16 / V>(a, p, s);
-  if (p.team == 32) return launch_layernorm_t<T, COPY, kWarpTeam, 8 / V>(a, p, s);
-  return launch_layernorm_t<T, COPY, kCtaTeam, 8 / V>(a, p, s);
+  constexpr int kMost = COPY && sizeof(T) == 2 ? kNormFwdCopyPieces : kNormFwdPieces;
+  constexpr int kOneCta = kNormFwdOneCtaBytes / static_cast<int>(sizeof(T));  // columns
+  constexpr int kSlice = COPY && sizeof(T) == 2 ? kOneCta / 2 : kOneCta;      // of a CTA in a cluster
+  constexpr int kMaxSplit = (kNormMaxK + kSlice - 1) / kSlice;
+  static_assert(kMaxSplit <= 8 && kMaxSplit * ((kSlice / V + 32 * kMost - 1) / (32 * kMost)) <= kNormMaxWarpSums,
+                "a portable cluster takes the longest row, and its warps' sums have a place each");
+  const int split = a.K <= kOneCta ? 1 : (a.K + kSlice - 1) / kSlice;
+  const int cols = ((a.K / 64 + split - 1) / split) * 64;
+  const int pieces = cols / V;
+  const int c = split > 1 ? kMost : pieces_per_thread(pieces, kMost);
+  const int team = (pieces + 32 * c - 1) / (32 * c) * 32;
+  const int mode = split > 1 ? kClusterTeam : team > 32 ? kCtaTeam : kWarpTeam;
+#define BN_LN(C)                                                                                     \
+  if constexpr (C <= kMost) {                                                                        \
+    if (c == C && mode == kWarpTeam) return launch_layernorm_t<T, COPY, kWarpTeam, C>(a, 1, cols, team, s); \
+    if (c == C && mode == kCtaTeam) return launch_layernorm_t<T, COPY, kCtaTeam, C>(a, 1, cols, team, s);   \
+    if (c == C) return launch_layernorm_t<T, COPY, kClusterTeam, C>(a, (a.K + cols - 1) / cols, cols, team, s); \
+  }
+  BN_LN(1) BN_LN(2) BN_LN(3) BN_LN(4)
+#undef BN_LN
+  return cudaErrorInvalidValue;
 }
 
 template <typename T, bool COPY, bool RMS, int MODE, int C, int R>

@@ -130,12 +130,12 @@ __global__ void __launch_bounds__(kNormBwdThreads)
     if (rows > R) fill(R, 1);
   }
 
-  Piece<T> gain[C];
+  // The gain of this thread's columns, in its own places behind the rings.
+  const uint32_t s_gain = smem_addr(smem) + nteams * 2 * R * row_bytes + 16 * tid;
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    unpack_piece(piece_or(static_cast<const T*>(a.gain) + col0 + (t + j * team) * V, a.gain != nullptr && ok[j], 1.0f),
-                 gain[j]);
-  }
+  for (int j = 0; j < C; ++j)
+    sts128(s_gain + 16 * j * nthr,
+           piece_or(static_cast<const T*>(a.gain) + col0 + (t + j * team) * V, a.gain != nullptr && ok[j], 1.0f));
 
   // Of the next batch: layer norm's statistics, row r's in the lanes of its
   // sums, and the scales of the 8-bit copy.
@@ -203,37 +203,46 @@ __global__ void __launch_bounds__(kNormBwdThreads)
     if (dead < 0 && !mbar_wait_idle(&my_full[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
     const int base = (b & 1) * R * row_bytes;
 
-    float sums[NV];
+    uint64_t s0[R], s1[R], r2[R], c2[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      sums[2 * r] = sums[2 * r + 1] = 0.0f;
-      if (r == 0 || row + r < rows) {
-        const float rr = RMS ? 0.0f : __shfl_sync(0xffffffffu, rstd, 2 * kLanes * r);
-        const float cc = RMS ? 0.0f : __shfl_sync(0xffffffffu, shift, 2 * kLanes * r);
-        const uint64_t r2 = f2(rr, rr), c2 = f2(cc, cc);
-        uint64_t s0 = 0, s1 = 0;
+      s0[r] = s1[r] = 0;
+      const float rr = RMS ? 0.0f : __shfl_sync(0xffffffffu, rstd, 2 * kLanes * r);
+      const float cc = RMS ? 0.0f : __shfl_sync(0xffffffffu, shift, 2 * kLanes * r);
+      r2[r] = f2(rr, rr);
+      c2[r] = f2(cc, cc);
+    }
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
+    for (int j = 0; j < C; ++j) {
+      Piece<T> gain;
+      unpack_piece(lds128_again(s_gain + 16 * j * nthr), gain);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r == 0 || row + r < rows) {
           Piece<T> d, x;
           values(base + r * row_bytes, j, COPY ? scale[COPY ? r : 0][j] : 0.0f, d, x);
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) {
-            const uint64_t tt = f2_mul(d.p[i], gain[j].p[i]);
+            const uint64_t tt = f2_mul(d.p[i], gain.p[i]);
             if constexpr (RMS) {
-              s0 = f2_fma(x.p[i], x.p[i], s0);
-              s1 = f2_fma(tt, x.p[i], s1);
+              s0[r] = f2_fma(x.p[i], x.p[i], s0[r]);
+              s1[r] = f2_fma(tt, x.p[i], s1[r]);
             } else {
-              const uint64_t nn = f2_fma(x.p[i], r2, c2);
-              s0 = f2_add(s0, tt);
-              s1 = f2_fma(tt, nn, s1);
+              const uint64_t nn = f2_fma(x.p[i], r2[r], c2[r]);
+              s0[r] = f2_add(s0[r], tt);
+              s1[r] = f2_fma(tt, nn, s1[r]);
               acc_g[j][i] = f2_fma(d.p[i], nn, acc_g[j][i]);
               acc_b[j][i] = f2_add(acc_b[j][i], d.p[i]);
             }
           }
         }
-        sums[2 * r] = f2_lo(s0) + f2_hi(s0);
-        sums[2 * r + 1] = f2_lo(s1) + f2_hi(s1);
       }
+    }
+    float sums[NV];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sums[2 * r] = f2_lo(s0[r]) + f2_hi(s0[r]);
+      sums[2 * r + 1] = f2_lo(s1[r]) + f2_hi(s1[r]);
     }
 
     // the team's sums: value i in the kLanes lanes from i * kLanes on
@@ -279,33 +288,41 @@ __global__ void __launch_bounds__(kNormBwdThreads)
       row_a = shift * row_b - rstd * (k * inv_k);
       row_b *= rstd;
     }
+    uint64_t a2[R], b2[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (r == 0 || row + r < rows) {
-        const float rr = __shfl_sync(0xffffffffu, row_r, 2 * kLanes * r);
-        const float bb = __shfl_sync(0xffffffffu, row_b, 2 * kLanes * r);
-        const float aa = RMS ? 0.0f : __shfl_sync(0xffffffffu, row_a, 2 * kLanes * r);
-        const uint64_t r2 = f2(rr, rr), a2 = f2(aa, aa), b2 = f2(bb, bb);
+      const float rr = __shfl_sync(0xffffffffu, row_r, 2 * kLanes * r);
+      const float bb = __shfl_sync(0xffffffffu, row_b, 2 * kLanes * r);
+      const float aa = RMS ? 0.0f : __shfl_sync(0xffffffffu, row_a, 2 * kLanes * r);
+      r2[r] = f2(rr, rr);
+      b2[r] = f2(bb, bb);
+      a2[r] = f2(aa, aa);
+    }
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
+    for (int j = 0; j < C; ++j) {
+      Piece<T> gain;
+      unpack_piece(lds128_again(s_gain + 16 * j * nthr), gain);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r == 0 || row + r < rows) {
           Piece<T> d, x, o;
           values(base + r * row_bytes, j, COPY ? scale[COPY ? r : 0][j] : 0.0f, d, x);
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) {
-            const uint64_t tt = f2_mul(d.p[i], gain[j].p[i]);
+            const uint64_t tt = f2_mul(d.p[i], gain.p[i]);
             if constexpr (RMS) {
-              const uint64_t nn = f2_mul(x.p[i], r2);
+              const uint64_t nn = f2_mul(x.p[i], r2[r]);
               acc_g[j][i] = f2_fma(nn, d.p[i], acc_g[j][i]);
-              o.p[i] = f2_fma(tt, r2, f2_mul(nn, b2));
+              o.p[i] = f2_fma(tt, r2[r], f2_mul(nn, b2[r]));
             } else {
-              o.p[i] = f2_fma(tt, r2, f2_fma(x.p[i], b2, a2));
+              o.p[i] = f2_fma(tt, r2[r], f2_fma(x.p[i], b2[r], a2[r]));
             }
           }
-          if (ok[j]) *reinterpret_cast<uint4*>(dx + j * team * V) = pack_piece(o);
+          if (ok[j]) *reinterpret_cast<uint4*>(dx + r * step + j * team * V) = pack_piece(o);
         }
-        dx += step;
       }
     }
+    dx += R * step;
 
     // every thread of the team is done with the stage
     if constexpr (MODE == kWarpTeam) __syncwarp();
@@ -367,10 +384,10 @@ __global__ void __launch_bounds__(kNormBwdThreads)
   pdl_launch_dependents();
 }
 
-// Shared memory of a CTA: the rings, reused for the teams' column sums.
+// Shared memory of a CTA: the rings and the gain, reused for the teams' column sums.
 template <typename T, bool COPY, int C, int R>
 inline int norm_bwd_smem_bytes(int teams, int team, int cols) {
-  const int ring = teams * 2 * R * norm_bwd_row_bytes<T, COPY, C>(team);
+  const int ring = teams * (2 * R * norm_bwd_row_bytes<T, COPY, C>(team) + 16 * C * team);
   const int sums = (teams - 1) * 2 * cols * 4;
   return ring > sums ? ring : sums;
 }

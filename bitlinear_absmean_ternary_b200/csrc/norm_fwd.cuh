@@ -5,27 +5,31 @@
 // part of a CTA, a CTA or a cluster of CTAs) walks the rows u, u + U, ...; rows
 // stream into shared memory by bulk copies, a batch of two rows ahead of the
 // batch at work; each thread takes its C pieces of 16 bytes into registers
-// once, and keeps its columns' gain and bias there for all rows.
+// once; its columns' gain and bias stay in shared memory for all rows.  A batch
+// costs a warp about 270 instructions whatever its lanes hold, the values about
+// 7.5 each, so C is as large as divides the row well (with 16 columns per thread
+// M = 2048, K = 21504 took 41.0 us, with 32 34.4: 0.80 of measured HBM).
 //
-// One stage of sums.  A warp sums x - p and (x - p)^2, p the mean of its first
+// One stage of sums.  A warp sums x and (x - p)^2, p the mean of its first
 // piece, and makes of them its sum S_w and the squares about its own mean
 //
-//   Q_w = sum (x - p)^2 - (sum (x - p))^2 / n_w.
+//   Q_w = sum (x - p)^2 - (S_w - n_w p)^2 / n_w.
 //
-// The n_p values behind p alone have squares n_p (p - mean_w)^2 about mean_w, so
-// the first term is at most 1 + n_w / n_p times Q_w and little cancels, whatever
-// the row's mean (with a mean of 1000 deviations, or an outlier in the piece
-// itself).  The team joins the warps' the same way about the first warp's mean:
+// The V values behind p alone have squares V (p - mean_w)^2 about mean_w, so the
+// first term is at most 1 + n_w / V times Q_w even with an outlier among them,
+// and about Q_w for others, whatever the row's mean: little cancels.  The team
+// joins the warps' about the first warp's mean c = S_0 / n_0:
 //
-//   d_w = S_w / n_w - S_0 / n_0,  mean = S_0 / n_0 + sum n_w d_w / K
-//   K var = sum (Q_w + n_w d_w^2) - (sum n_w d_w)^2 / K
+//   mean = sum S_w / K,  K var = sum (Q_w + n_w (S_w / n_w - c)^2) - K (mean - c)^2
 //
 // In a cluster the warps' sums travel by st.async, as in the backward kernel.
 //
-// Other forms measured for M = 2048, K = 21504 (M = 4096, K = 2560): a CTA per
+// Other forms measured at M = 2048, K = 21504 (M = 4096, K = 2560): a CTA per
 // row that reads it three times from L1 or L2 41 us (16.2); a row in the
-// registers of up to 896 threads 60 (19), of few threads with 80 columns each
-// 77 (14.4); this one XX (YY).
+// registers of up to 896 threads 60 (19), or of few threads with 80 columns each
+// 77 (14.4); the sums of a batch exchanged while the batch before is finished
+// 43.7 (12.7); this one 34.4 (10.7).  Short calls (M = 4, K = 256: 1.7 us) are a
+// launch and a trip to memory.
 #pragma once
 
 #include "norm.cuh"
@@ -54,7 +58,8 @@ constexpr int kNormFwdMaxTeams = 16;  // of a CTA
 // kClusterTeam).  cols: columns per CTA, a multiple of 64 (the last of a
 // cluster may have fewer).
 template <typename T, bool COPY, int MODE, int C>
-__global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFwd a, int team, int split, int cols) {
+__global__ void __launch_bounds__(kNormFwdThreads, 1)
+    layernorm_kernel(const NormFwd a, int team, int split, int cols) {
   constexpr int V = Piece<T>::V, R = 2;
   constexpr int kEntries = MODE == kClusterTeam ? kNormMaxWarpSums : 16;
   constexpr int kPerLane = MODE == kClusterTeam ? 2 : 1;  // entries a lane joins
@@ -138,12 +143,14 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
     if (rows > 0) fill(0, 0);
     if (rows > R) fill(R, 1);
   }
-  uint4 g[C], h[C];
+  // Gain and bias of this thread's columns, in its own places behind the rings.
+  const int nthr = static_cast<int>(blockDim.x);
+  const uint32_t s_gain = smem_addr(smem) + nteams * 2 * R * row_bytes + 16 * tid, s_bias = s_gain + 16 * C * nthr;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int c = col0 + (t + j * team) * V;
-    g[j] = piece_or(static_cast<const T*>(a.gain) + c, a.gain != nullptr && ok[j], 1.0f);
-    h[j] = piece_or(static_cast<const T*>(a.bias) + c, a.bias != nullptr && ok[j], 0.0f);
+    sts128(s_gain + 16 * j * nthr, piece_or(static_cast<const T*>(a.gain) + c, a.gain != nullptr && ok[j], 1.0f));
+    sts128(s_bias + 16 * j * nthr, piece_or(static_cast<const T*>(a.bias) + c, a.bias != nullptr && ok[j], 0.0f));
   }
 
   const float inv_k = 1.0f / static_cast<float>(a.K);
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
           const uint64_t d = f2_add(x.p[i], p2);
-          t0 = f2_add(t0, d);
+          t0 = f2_add(t0, x.p[i]);
           t1 = f2_fma(d, d, t1);
         }
         if (ok[j]) {
@@ -194,8 +201,8 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
       sums[2 * r + 1] = f2_lo(s1) + f2_hi(s1);
     }
     float k = warp_sums(sums, lane);
-    const float other = __shfl_xor_sync(0xffffffffu, k, 8);  // the S of a Q's lanes
-    k = lane & 8 ? k - other * other * inv_mine : k + n_mine * (lane & 16 ? pivot[1] : pivot[0]);
+    const float off = __shfl_xor_sync(0xffffffffu, k, 8) - n_mine * (lane & 16 ? pivot[1] : pivot[0]);
+    if (lane & 8) k -= off * off * inv_mine;
 
     float mean[R], var[R];
     if constexpr (MODE == kWarpTeam) {
@@ -228,17 +235,17 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
         if (n_of[i] > 0.0f) {
           const float4 e = buf[lane + 32 * i];
           const float d0 = e.x * inv_of[i] - m0, d1 = e.z * inv_of[i] - m1;
-          sums[0] += n_of[i] * d0;
+          sums[0] += e.x;
           sums[1] += e.y + n_of[i] * d0 * d0;
-          sums[2] += n_of[i] * d1;
+          sums[2] += e.z;
           sums[3] += e.w + n_of[i] * d1 * d1;
         }
       }
       k = warp_sums(sums, lane);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float d = __shfl_sync(0xffffffffu, k, 16 * r) * inv_k;
-        mean[r] = (r == 0 ? m0 : m1) + d;
+        mean[r] = __shfl_sync(0xffffffffu, k, 16 * r) * inv_k;
+        const float d = mean[r] - (r == 0 ? m0 : m1);
         var[r] = __shfl_sync(0xffffffffu, k, 16 * r + 8) * inv_k - d * d;
       }
     }
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
 
     float rstd[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) rstd[r] = rsqrtf(fmaxf(var[r], 0.0f) + a.eps);
+    for (int r = 0; r < R; ++r) rstd[r] = rsqrtf((var[r] < 0.0f ? 0.0f : var[r]) + a.eps);  // NaN stays NaN
     const bool two = row + 1 < rows;
     if (t == 0 && rank == 0) {
 #pragma unroll
@@ -263,8 +270,8 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       Piece<T> gg, hh;
-      unpack_piece(g[j], gg);
-      unpack_piece(h[j], hh);
+      unpack_piece(lds128_again(s_gain + 16 * j * nthr), gg);
+      unpack_piece(lds128_again(s_bias + 16 * j * nthr), hh);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint64_t m2 = f2(-mean[r], -mean[r]), r2 = f2(rstd[r], rstd[r]);
@@ -277,18 +284,13 @@ __global__ void __launch_bounds__(kNormFwdThreads) layernorm_kernel(const NormFw
       }
     }
     if constexpr (COPY) {
-      uint4 p[R * C];
-      int64_t p_at[R * C];
-      bool present[R * C];
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
+        bool present[C];
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          p[r * C + j] = raw[r][j];
-          p_at[r * C + j] = at + r * step + j * team * V;
-          present[r * C + j] = ok[j] && (r == 0 || two);
-        }
-      store_act8_pieces<T>(p, p_at, present, a.x8, a.x_scale, lane);
+        for (int j = 0; j < C; ++j) present[j] = ok[j] && (r == 0 || two);
+        store_act8_pieces<T>(raw[r], at + r * step, team * V, present, a.x8, a.x_scale, lane);
+      }
     }
     at += R * step;
   }

@@ -109,6 +109,10 @@ BN_DEV uint32_t lds32_again(uint32_t addr) {
   return v;
 }
 
+BN_DEV void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // mbar_wait and mbar_wait_cluster for many warps that wait together: a try
 // suspends its warp for up to 20 us, so waiting takes no issue slots from the
 // warps at work.
