@@ -13,19 +13,15 @@ using namespace bitnet_host;
 
 constexpr int64_t kNormMaxK = 32768;
 
-// How a backward pass deals out its columns (measured, us a call in a graph):
-// 8 columns per thread up to K = 1024 (M = 4096, K = 640: 9.3 against 10.9 with
-// 16, M = 333 f32: 4.8 against 5.8), 16 beyond; a CTA per row up to K = 4096
-// and a cluster of CTAs of at most 256 threads beyond (M = 2048, K = 5376: 19.6
-// against 20.2 in one CTA; M = 4096, K = 6912: 36.9 against 40.5).
-constexpr int64_t kNormNarrowK = 1024;
-constexpr int64_t kNormOneCtaK = 4096;
-constexpr int kNormClusterThreads = 256;
-// CTAs per SM, at most.  A CTA without a cluster holds several teams up to 512
-// threads, so one per SM is enough, and leaves fewer partial rows to join
-// (M = 4096, K = 2560: 21.1 us with three CTAs per SM, 18.9 with three teams).
-constexpr int kNormCtasPerSm = 1;
-constexpr int kNormClusterCtasPerSm = 4;
+// Backward passes: a CTA per row up to kNormBwdOneCtaK columns (4096 in fp32), a
+// cluster of CTAs of at most kNormBwdSliceK columns beyond (M = 4096, K = 6912
+// RMSNorm 33.2 us as two CTAs, 35.0 as one; M = 2048, K = 5376 layer norm 19.2
+// in one CTA, 19.9 in two).  Up to three 16-byte pieces per thread of bf16
+// (M = 2048, K = 21504: layer norm 56.6 us with two, 53.2 with three; RMSNorm
+// 51.7 with two, 49.2 with three or four), four of fp32.
+constexpr int kNormBwdOneCtaK = 6144;
+constexpr int kNormBwdSliceK = 4096;
+constexpr int kNormBwdPieces = 3;
 // Layer norm forward: a CTA per row of up to 16 KB, a cluster beyond, whose CTAs
 // take up to 16 KB of the row each, or 8 KB where bf16 rows leave an 8-bit copy
 // (M = 2048, K = 21504 with the copy 54.7 us against 60.9; without it 34.4
@@ -55,35 +51,19 @@ int kernel_registers(F* fn, std::atomic<int> (&cache)[kMaxDevices]) {
   return n;
 }
 
-// How the columns of a row are dealt out: independent of the types, as the
-// backward passes' workspace follows from it.
-struct NormPlan {
-  int cv;     // columns per thread
-  int split;  // CTAs (a cluster) per row
-  int cols;   // columns per CTA
-  int team;   // threads per row and CTA
-};
+// Partial rows of column sums that a backward pass leaves at most.
+int64_t norm_most_parts(int64_t M) { return std::min<int64_t>(M, sm_count()); }
 
-NormPlan norm_plan(int64_t K) {
-  NormPlan p;
-  p.cv = K <= kNormNarrowK ? 8 : 16;
-  const int64_t want = (K + p.cv - 1) / p.cv;
-  p.split = K <= kNormOneCtaK ? 1 : static_cast<int>((want + kNormClusterThreads - 1) / kNormClusterThreads);
-  p.cols = static_cast<int>((K / 64 + p.split - 1) / p.split) * 64;
-  p.split = static_cast<int>((K + p.cols - 1) / p.cols);
-  p.team = (((p.cols + p.cv - 1) / p.cv) + 31) / 32 * 32;
-  return p;
+// 16-byte pieces per thread, least to most: the most that leave at most a
+// twelfth of the team's places empty, as empty places cost like full ones.
+int pieces_per_thread(int pieces, int least, int most) {
+  for (int c = most; c > least; --c) {
+    const int places = (pieces + 32 * c - 1) / (32 * c) * 32 * c;
+    if (12 * (places - pieces) <= pieces) return c;
+  }
+  return least;
 }
 
-// Clusters (CTAs when split is 1) that a pass uses at most.
-int64_t norm_most_parts(const NormPlan& p, int64_t M) {
-  const int64_t ctas = static_cast<int64_t>(sm_count()) * (p.split > 1 ? kNormClusterCtasPerSm : kNormCtasPerSm);
-  return std::min<int64_t>(M, ctas / p.split);
-}
-
-// Clusters of this launch that run at the same time (GPCs hold a whole number
-// of them, so it can be less than the SMs would suggest); the last answer is
-// kept per kernel and device as (key << 16 | answer).
 template <typename F>
 int64_t active_clusters(F* fn, const cudaLaunchConfig_t& cfg, int split, std::atomic<uint64_t> (&cache)[kMaxDevices]) {
   const int d = current_device();
@@ -151,16 +131,6 @@ cudaError_t launch_layernorm_t(const NormFwd& a, int split, int cols, int team, 
                             split, cols);
 }
 
-// Pieces per thread: the most that leave at most an eighth of the team's
-// places empty.
-int pieces_per_thread(int pieces, int most) {
-  for (int c = most; c > 1; --c) {
-    const int places = (pieces + 32 * c - 1) / (32 * c) * 32 * c;
-    if (8 * (places - pieces) <= pieces) return c;
-  }
-  return 1;
-}
-
 template <typename T, bool COPY>
 cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
   constexpr int V = Piece<T>::V;
@@ -173,7 +143,7 @@ cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
   const int split = a.K <= kOneCta ? 1 : (a.K + kSlice - 1) / kSlice;
   const int cols = ((a.K / 64 + split - 1) / split) * 64;
   const int pieces = cols / V;
-  const int c = split > 1 ? kMost : pieces_per_thread(pieces, kMost);
+  const int c = split > 1 ? kMost : pieces_per_thread(pieces, 1, kMost);
   const int team = (pieces + 32 * c - 1) / (32 * c) * 32;
   const int mode = split > 1 ? kClusterTeam : team > 32 ? kCtaTeam : kWarpTeam;
 #define BN_LN(C)                                                                                     \
@@ -188,20 +158,19 @@ cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
 }
 
 template <typename T, bool COPY, bool RMS, int MODE, int C, int R>
-cudaError_t launch_norm_bwd(const NormBwd& a, const NormPlan& p, cudaStream_t s) {
+cudaError_t launch_norm_bwd(const NormBwd& a, int split, int cols, int team, cudaStream_t s) {
   static std::atomic<bool> done[kMaxDevices] = {};
   static std::atomic<int> regs[kMaxDevices] = {};
   static std::atomic<uint64_t> active[kMaxDevices] = {};
   auto kern = norm_bwd_kernel<T, COPY, RMS, MODE, C, R>;
-  int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(kNormMaxTeams, kNormBwdThreads / p.team));
-  while (teams > 1 && norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols) > kNormSmemMax) --teams;
-  const int threads = teams * p.team;
-  const int smem = norm_bwd_smem_bytes<T, COPY, C, R>(teams, p.team, p.cols);
+  int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(kNormMaxTeams, kNormBwdThreads / team));
+  while (teams > 1 && norm_bwd_smem_bytes<T, COPY, C, R>(teams, team, cols) > kNormSmemMax) --teams;
+  const int smem = norm_bwd_smem_bytes<T, COPY, C, R>(teams, team, cols);
   cudaError_t e = set_smem(kern, kNormSmemMax, done);
   if (e != cudaSuccess) return e;
-  int64_t parts = std::min(norm_most_parts(p, a.M), (a.M + teams - 1) / teams);
-  e = launch_teams<MODE>(kern, p.split, threads, smem, parts, kernel_registers(kern, regs), active, s, a, p.team,
-                         p.split, p.cols);
+  int64_t parts = std::min(norm_most_parts(a.M), (a.M + teams - 1) / teams);
+  e = launch_teams<MODE>(kern, split, teams * team, smem, parts, kernel_registers(kern, regs), active, s, a, team,
+                         split, cols);
   if (e != cudaSuccess || parts == 1 || (a.dgain == nullptr && a.dbias == nullptr)) return e;
   return launch_pdl(norm_join_kernel, dim3(static_cast<unsigned>(a.K / (4 * kNormJoinLanes)), a.dbias != nullptr ? 2 : 1),
                     dim3(kNormJoinThreads), 0, s, static_cast<const float*>(a.part), static_cast<int>(parts), a.K,
@@ -211,18 +180,30 @@ cudaError_t launch_norm_bwd(const NormBwd& a, const NormPlan& p, cudaStream_t s)
 template <typename T, bool COPY, bool RMS>
 cudaError_t launch_norm_backward_t(const NormBwd& a, cudaStream_t s) {
   constexpr int V = Piece<T>::V;
-  static_assert(kNormNarrowK <= kNormOneCtaK && kNormNarrowK <= 8 * kNormBwdThreads &&
-                    kNormOneCtaK <= 16 * kNormBwdThreads,
-                "a CTA takes a whole row");
-  static_assert(kNormMaxK <= 8 * 16 * kNormClusterThreads && kNormClusterThreads / 32 * 8 <= kNormMaxWarpSums,
-                "a portable cluster takes the longest row");
-  // four rows a batch where they are small (8-bit copies in clusters: M = 4096,
-  // K = 6912 36.2 us against 39.2 with two)
-  const NormPlan p = norm_plan(a.K);
-  if (p.split > 1) return launch_norm_bwd<T, COPY, RMS, kClusterTeam, 16 / V, COPY && sizeof(T) == 2 ? 4 : 2>(a, p, s);
-  if (p.cv == 16) return launch_norm_bwd<T, COPY, RMS, kCtaTeam, 16 / V, 2>(a, p, s);
-  if (p.team == 32) return launch_norm_bwd<T, COPY, RMS, kWarpTeam, 8 / V, 4>(a, p, s);
-  return launch_norm_bwd<T, COPY, RMS, kCtaTeam, 8 / V, 4>(a, p, s);
+  constexpr int kMost = sizeof(T) == 4 ? 4 : kNormBwdPieces;
+  constexpr int kLeast = sizeof(T) == 4 ? 4 : 2;  // in a cluster
+  constexpr int kOneCta = sizeof(T) == 4 ? kNormBwdSliceK : kNormBwdOneCtaK;
+  constexpr int kMaxSplit = (kNormMaxK + kNormBwdSliceK - 1) / kNormBwdSliceK;
+  static_assert(kMaxSplit <= 8 && kMaxSplit * (kNormBwdSliceK / V / (32 * kLeast)) <= kNormMaxWarpSums,
+                "a portable cluster takes the longest row, and its warps' sums have a place each");
+  const int split = a.K <= kOneCta ? 1 : (a.K + kNormBwdSliceK - 1) / kNormBwdSliceK;
+  const int cols = (a.K / 64 + split - 1) / split * 64;
+  const int pieces = cols / V;
+  const int c = pieces_per_thread(pieces, split > 1 ? kLeast : 1, kMost);
+  const int team = (pieces + 32 * c - 1) / (32 * c) * 32;
+  // rows of a batch: four where a thread has few values of a row
+#define BN_NB(C)                                                                                                     \
+  if constexpr (C <= kMost) {                                                                                        \
+    constexpr int R = C * V <= 8 || (COPY && C * V <= 16 && sizeof(T) == 2) ? 4 : 2;                                 \
+    if (c == C && split == 1 && team == 32) return launch_norm_bwd<T, COPY, RMS, kWarpTeam, C, R>(a, 1, cols, team, s); \
+    if (c == C && split == 1) return launch_norm_bwd<T, COPY, RMS, kCtaTeam, C, R>(a, 1, cols, team, s);             \
+    if constexpr (C >= kLeast)                                                                                       \
+      if (c == C)                                                                                                    \
+        return launch_norm_bwd<T, COPY, RMS, kClusterTeam, C, R>(a, (a.K + cols - 1) / cols, cols, team, s);         \
+  }
+  BN_NB(1) BN_NB(2) BN_NB(3) BN_NB(4)
+#undef BN_NB
+  return cudaErrorInvalidValue;
 }
 
 template <bool RMS>
@@ -273,7 +254,7 @@ bitnet_status bitnet_layernorm(const void* x, int dtype, int64_t M, int64_t K, c
 
 size_t bitnet_norm_backward_workspace_bytes(int64_t M, int64_t K) {
   if (!valid_rows(M, K)) return 0;
-  return 2 * static_cast<size_t>(norm_most_parts(norm_plan(K), M)) * static_cast<size_t>(K) * sizeof(float);
+  return 2 * static_cast<size_t>(norm_most_parts(M)) * static_cast<size_t>(K) * sizeof(float);
 }
 
 bitnet_status bitnet_layernorm_backward(const void* dy, int dtype, int64_t M, int64_t K, const void* x,
