@@ -1,7 +1,8 @@
 // Host side of the BitLinear C ABI declared in include/bitnet.h: the weight
 // packs (absmean ternarisation, pack.cuh), the pack without allocation, and
 // the status calls.  The other entry points live beside their kernels:
-// k_quant.cu, k_gemv.cu, k_gemm.cu, k_ffn.cu, k_b3.cu and k_ste.cu.
+// k_quant.cu, k_gemv.cu, k_gemm.cu, k_ffn.cu, k_b3.cu, k_ste.cu, k_norm.cu and
+// k_act8.cu.
 #include "host_common.h"
 #include "pack.cuh"
 
@@ -148,7 +149,7 @@ bitnet_status bitnet_get_device_status(void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return BITNET_ERR_CUDA;
   cudaError_t (*const takers[])(unsigned int*) = {take_error_gemv, take_error_gemm, take_error_gemm_fused,
                                                   take_error_ffn,  take_error_b3,   take_error_ste,
-                                                  take_error_quant};
+                                                  take_error_quant, take_error_norm};
   bool timed_out = false;
   for (auto take : takers) {
     unsigned int v = 0;

@@ -154,6 +154,7 @@ cudaError_t take_error_ffn(unsigned int* v);
 cudaError_t take_error_b3(unsigned int* v);
 cudaError_t take_error_ste(unsigned int* v);
 cudaError_t take_error_quant(unsigned int* v);
+cudaError_t take_error_norm(unsigned int* v);
 
 }  // namespace bitnet_host
 

@@ -31,7 +31,6 @@ constexpr int kNormBwdPieces = 3;
 constexpr int kNormFwdOneCtaBytes = 16384;
 constexpr int kNormFwdPieces = 4;
 constexpr int kNormFwdCopyPieces = 3;
-constexpr int kNormFwdTeamThreads = 512;  // several rows in a CTA up to this
 constexpr int kSmemPerSm = 233472;  // 228 KB
 constexpr int kNormSmemMax = 220 * 1024;
 
@@ -39,6 +38,7 @@ bool valid_rows(int64_t M, int64_t K) { return valid_k(K) && K <= kNormMaxK && M
 
 bool valid_eps(float eps) { return std::isfinite(eps) && eps > 0.0f; }
 
+// Registers per thread of a kernel, looked up once per device.
 template <typename F>
 int kernel_registers(F* fn, std::atomic<int> (&cache)[kMaxDevices]) {
   const int d = current_device();
@@ -55,8 +55,10 @@ int kernel_registers(F* fn, std::atomic<int> (&cache)[kMaxDevices]) {
 int64_t norm_most_parts(int64_t M) { return std::min<int64_t>(M, sm_count()); }
 
 // 16-byte pieces per thread, least to most: the most that leave at most a
-// twelfth of the team's places empty, as empty places cost like full ones.
+// twelfth of the team's places empty, as empty places cost like full ones; no
+// fewer than keep the team within 512 threads.
 int pieces_per_thread(int pieces, int least, int most) {
+  least = std::max(least, (pieces + kNormMaxThreads - 1) / kNormMaxThreads);
   for (int c = most; c > least; --c) {
     const int places = (pieces + 32 * c - 1) / (32 * c) * 32 * c;
     if (12 * (places - pieces) <= pieces) return c;
@@ -64,10 +66,15 @@ int pieces_per_thread(int pieces, int least, int most) {
   return least;
 }
 
+// Clusters of this launch that run at the same time: GPCs hold a whole number
+// of them, so it can be less than the SMs would suggest, and a grid of more runs
+// in two waves (M = 2048, K = 21504 106 us).  The last answer is kept per kernel
+// and device as key << 16 | answer.
 template <typename F>
 int64_t active_clusters(F* fn, const cudaLaunchConfig_t& cfg, int split, std::atomic<uint64_t> (&cache)[kMaxDevices]) {
   const int d = current_device();
-  const uint64_t key = (static_cast<uint64_t>(cfg.dynamicSmemBytes) << 16 | cfg.blockDim.x) << 4 | static_cast<uint64_t>(split);
+  const uint64_t key =
+      (static_cast<uint64_t>(cfg.dynamicSmemBytes) << 16 | cfg.blockDim.x) << 4 | static_cast<uint64_t>(split);
   if (d >= 0 && d < kMaxDevices) {
     const uint64_t c = cache[d].load(std::memory_order_relaxed);
     if (c >> 16 == key) return static_cast<int64_t>(c & 0xFFFF);
@@ -78,8 +85,9 @@ int64_t active_clusters(F* fn, const cudaLaunchConfig_t& cfg, int split, std::at
   return n;
 }
 
-// Grid of a kernel with a team per row: at most `most` clusters (CTAs), as many
-// as run at the same time, and the launch.
+// Launches a kernel with a team per row on at most `clusters` clusters (CTAs
+// where MODE is not kClusterTeam), no more than run at the same time, and leaves
+// there how many it took.
 template <int MODE, typename... KArgs, typename... Args>
 cudaError_t launch_teams(void (*kern)(KArgs...), int split, int threads, int smem, int64_t& clusters, int registers,
                          std::atomic<uint64_t> (&cache)[kMaxDevices], cudaStream_t s, Args... args) {
@@ -121,7 +129,7 @@ cudaError_t launch_layernorm_t(const NormFwd& a, int split, int cols, int team, 
   const int teams = MODE == kClusterTeam
                         ? 1
                         : static_cast<int>(std::max<int64_t>(
-                              1, std::min<int64_t>({most, kNormFwdTeamThreads / team, kNormSmemMax / team_smem,
+                              1, std::min<int64_t>({most, kNormMaxThreads / team, kNormSmemMax / team_smem,
                                                     (a.M + sm_count() - 1) / sm_count()})));
   const int smem = teams * team_smem;
   const cudaError_t e = set_smem(kern, kNormSmemMax, done);
@@ -163,7 +171,7 @@ cudaError_t launch_norm_bwd(const NormBwd& a, int split, int cols, int team, cud
   static std::atomic<int> regs[kMaxDevices] = {};
   static std::atomic<uint64_t> active[kMaxDevices] = {};
   auto kern = norm_bwd_kernel<T, COPY, RMS, MODE, C, R>;
-  int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(kNormMaxTeams, kNormBwdThreads / team));
+  int teams = MODE == kClusterTeam ? 1 : std::max(1, std::min(kNormMaxTeams, kNormMaxThreads / team));
   while (teams > 1 && norm_bwd_smem_bytes<T, COPY, C, R>(teams, team, cols) > kNormSmemMax) --teams;
   const int smem = norm_bwd_smem_bytes<T, COPY, C, R>(teams, team, cols);
   cudaError_t e = set_smem(kern, kNormSmemMax, done);
@@ -189,8 +197,14 @@ cudaError_t launch_norm_backward_t(const NormBwd& a, cudaStream_t s) {
   const int split = a.K <= kOneCta ? 1 : (a.K + kNormBwdSliceK - 1) / kNormBwdSliceK;
   const int cols = (a.K / 64 + split - 1) / split * 64;
   const int pieces = cols / V;
-  const int c = pieces_per_thread(pieces, split > 1 ? kLeast : 1, kMost);
-  const int team = (pieces + 32 * c - 1) / (32 * c) * 32;
+  int c = pieces_per_thread(pieces, split > 1 ? kLeast : 1, kMost);
+  int team = (pieces + 32 * c - 1) / (32 * c) * 32;
+  if constexpr (sizeof(T) == 4) {  // the ring of four-row batches can exceed a CTA's shared memory
+    if (c == 2 && norm_bwd_smem_bytes<T, COPY, 2, 4>(1, team, cols) > kNormSmemMax) {
+      c = 3;
+      team = (pieces + 32 * c - 1) / (32 * c) * 32;
+    }
+  }
   // rows of a batch: four where a thread has few values of a row
 #define BN_NB(C)                                                                                                     \
   if constexpr (C <= kMost) {                                                                                        \
@@ -232,6 +246,8 @@ bitnet_status check_norm_backward(const void* dy, int dtype, int64_t M, int64_t 
 }
 
 }  // namespace
+
+BITNET_DEFINE_TAKE_ERROR(norm)
 
 extern "C" {
 

@@ -23,6 +23,7 @@ namespace bitnet {
 // Who owns a row: a warp, part or all of a CTA, or a cluster of CTAs.
 enum NormTeam { kWarpTeam, kCtaTeam, kClusterTeam };
 
+constexpr int kNormMaxThreads = 512;  // of a CTA
 constexpr int kNormMaxWarpSums = 64;  // warps of a team over its cluster
 
 struct NormBwd {

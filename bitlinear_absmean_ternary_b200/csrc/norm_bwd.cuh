@@ -32,7 +32,6 @@ namespace bitnet {
 
 // ---------------------------------------------------------------- kernel
 
-constexpr int kNormBwdThreads = 512;  // at most
 constexpr int kNormMaxTeams = 8;      // of a CTA
 // Bytes of a row in the ring: dy, then x or its codes, each for all of the
 // team's threads (what lies past the row's columns stays zero).
@@ -46,7 +45,7 @@ __host__ __device__ constexpr int norm_bwd_row_bytes(int team) {
 // kClusterTeam).  cols: columns per CTA, a multiple of 64 (the last of a
 // cluster may have fewer).
 template <typename T, bool COPY, bool RMS, int MODE, int C, int R>
-__global__ void __launch_bounds__(kNormBwdThreads)
+__global__ void __launch_bounds__(kNormMaxThreads)
     norm_bwd_kernel(const NormBwd a, int team, int split, int cols) {
   constexpr int V = Piece<T>::V;
   constexpr int NV = 2 * R, kLanes = 32 / NV;  // sums of a batch, lanes that hold each

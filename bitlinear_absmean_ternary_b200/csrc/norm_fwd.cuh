@@ -50,7 +50,6 @@ struct NormFwd {
   int K;
 };
 
-constexpr int kNormFwdThreads = 512;  // at most
 constexpr int kNormFwdMaxTeams = 16;  // of a CTA
 
 // team: threads per row and CTA (a multiple of 32; blockDim.x is a multiple of
@@ -58,7 +57,7 @@ constexpr int kNormFwdMaxTeams = 16;  // of a CTA
 // kClusterTeam).  cols: columns per CTA, a multiple of 64 (the last of a
 // cluster may have fewer).
 template <typename T, bool COPY, int MODE, int C>
-__global__ void __launch_bounds__(kNormFwdThreads, 1)
+__global__ void __launch_bounds__(kNormMaxThreads, 1)
     layernorm_kernel(const NormFwd a, int team, int split, int cols) {
   constexpr int V = Piece<T>::V, R = 2;
   constexpr int kEntries = MODE == kClusterTeam ? kNormMaxWarpSums : 16;

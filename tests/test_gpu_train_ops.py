@@ -302,6 +302,28 @@ def test_rmsnorm_backward(dev, M, K, dtype):
     check_norm_backward(dy, values64(x8, x_scale), zero, r, gain, dx, dgain, False, rel)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norms_at_every_width(dev, dtype):
+    """Every K the norms take, three rows each."""
+    M, zero = 3, torch.zeros(3, dtype=torch.float64, device=dev)
+    big_x, big_dy = tensor(dev, M, 32768, dtype, 5, shift=0.3), tensor(dev, M, 32768, dtype, 6, scale=0.01, loud=False)
+    big_g, big_b = vector(dev, 32768, dtype, 1), vector(dev, 32768, dtype, 2, -0.3, 0.3)
+    for K in range(64, 32768 + 64, 64):
+        x, dy, gain, bias = big_x[:, :K].contiguous(), big_dy[:, :K].contiguous(), big_g[:K], big_b[:K]
+        y, mean, rstd, x8, xs = bl.bitnet_layernorm(x, gain, bias, EPS, checkpoint=True)
+        check_layernorm(x, gain, bias, y, mean, rstd)
+        check_layernorm(x, gain, bias, *bl.bitnet_layernorm(x, gain, bias, EPS))
+        for a, b in zip((x8, xs), bl.bitnet_act_checkpoint(x)):
+            assert torch.equal(a, b), K
+        for form in ({"x": x}, {"x8": x8, "x_scale": xs}):
+            read = x.double() if "x" in form else values64(x8, xs)
+            got = bl.bitnet_layernorm_backward(dy, mean, rstd, gain=gain, **form)
+            check_norm_backward(dy, read, mean.double(), rstd.double(), gain, *got, zero)
+            r, rel = rms64(read)
+            check_norm_backward(dy, read, zero, r, gain, *bl.bitnet_rmsnorm_backward(dy, gain=gain, **form), False, rel)
+    assert bl.bitnet_get_device_status() == bl.BITNET_OK
+
+
 @pytest.mark.parametrize("M,K", [(5, 256), (300, 2560), (30, 21504)])
 def test_norm_backward_outputs_that_are_not_wanted(dev, M, K):
     x = tensor(dev, M, K, "bf16", 3)
