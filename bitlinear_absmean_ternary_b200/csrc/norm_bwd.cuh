@@ -11,7 +11,7 @@
 // first) and pass one team barrier; what else is wanted once per row is
 // computed for all rows of the batch at once, each in its lanes.  dy and x are
 // read from shared memory a second time for dx: kept in registers as fp32 they
-// leave too few warps per SM.
+// leave too few warps per SM.  The gain stays in shared memory for all rows.
 //
 // In a cluster every warp sends its sums to every CTA (st.async, counted by an
 // mbarrier of the receiver), so no fence waits for the stores of dx, as the
@@ -21,9 +21,12 @@
 // partial row per CTA (cluster), which norm_join_kernel adds in order; one
 // partial row alone is the result.
 //
-// Bound by memory for many rows (K = 2560 without the column sums: 0.94 of
-// measured HBM at M = 18944, 0.72 at M = 4096; RMSNorm at M = 2048, K = 21504
-// 51.7 us, 0.79), by the two launches and the join (about 4 us) for few.
+// Bound by memory for many rows (K = 2560 without the column sums: 49.1 us, 0.92
+// of measured HBM, at M = 18944; RMSNorm at M = 2048, K = 21504 48.9 us, 0.84),
+// below that by what a grid costs before its first batch and after its last,
+// about 4.5 us (K = 2560 without the sums 14.3 us, 0.68, at M = 4096), and by the
+// join, 3.5 us more.  8-bit copies save bytes but not time here (M = 2048,
+// K = 21504 RMSNorm 52.1 us): their codes take more instructions than bf16.
 #pragma once
 
 #include "norm.cuh"
@@ -103,9 +106,11 @@ __global__ void __launch_bounds__(kNormMaxThreads)
   pdl_wait();
   // Without a join behind it the next kernel may start its own prologue now;
   // with one, its CTAs would only take this kernel's place on the SMs
-  // (M = 4096, K = 2560: 19.0 us with the join let go here, 17.3 at the end).
+  // (M = 4096, K = 2560: 19.0 us with the join let go here, 17.3 at the end), as
+  // the next grid's clusters would (M = 4096, K = 6912 RMSNorm without dgain 39.9
+  // us let go here, 31.9 at the end).
   const bool joined = clusters > 1 && (a.dgain != nullptr || a.dbias != nullptr);
-  if (!joined) pdl_launch_dependents();
+  if (MODE != kClusterTeam && !joined) pdl_launch_dependents();
 
   const uint64_t once = policy_evict_first();
   const int64_t step = static_cast<int64_t>(U) * a.K;
