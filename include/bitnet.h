@@ -500,7 +500,10 @@ bitnet_status bitnet_bitlinear_ffn_gemv(const void* x, int x_dtype, int64_t M, i
  * fp32 in a fixed order, so a call repeated on the same device gives the same
  * bits; results are rounded once, when they are stored.  Outputs must not
  * overlap inputs or each other.  Scales and statistics need 4-byte alignment
- * only.  Asynchronous; nothing of a call survives it but its outputs.
+ * only.  Asynchronous; nothing of a call survives it but its outputs.  Every
+ * input is read after the previous kernel on the stream has completed.  The
+ * norms' waits on copies and on cluster peers are bounded and report
+ * BITNET_ERR_TIMEOUT through bitnet_get_device_status.
  *
  * The 8-bit copy of an M x K activation x: per row and group of 64 columns
  *
