@@ -179,6 +179,10 @@ cudaError_t launch_norm_bwd(const NormBwd& a, int split, int cols, int team, cud
   cudaError_t e = set_smem(kern, kNormSmemMax, done);
   if (e != cudaSuccess) return e;
   int64_t parts = std::min(norm_most_parts(a.M), (a.M + teams - 1) / teams);
+  // Rows for one batch of every team stay in one CTA, as the join costs more than
+  // the longer sums (layer norm of M = 32, K = 256 4.2 us, 3.7 so; of M = 4,
+  // K = 2560 5.7, 4.5 so; with a second batch M = 8, K = 2560 5.8, 6.1 so).
+  if (a.M <= R * teams) parts = 1;
   // A CTA for every SM: too much shared memory for a second one, which would go
   // where the grid before has left early (M = 16384, K = 256: 12.5 us; 10.6 so).
   if (MODE != kClusterTeam && 2 * parts > sm_count()) smem = std::max(smem, kSmemPerSm / 2);
