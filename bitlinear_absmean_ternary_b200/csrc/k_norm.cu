@@ -22,13 +22,15 @@ constexpr int64_t kNormMaxK = 32768;
 constexpr int kNormBwdOneCtaK = 6144;
 constexpr int kNormBwdSliceK = 4096;
 constexpr int kNormBwdPieces = 3;
-// Layer norm forward: a CTA per row of up to 16 KB, a cluster beyond, whose CTAs
-// take up to 16 KB of the row each, or 8 KB where bf16 rows leave an 8-bit copy
-// (M = 2048, K = 21504 with the copy 54.7 us against 60.9; without it 34.4
-// either way).  Up to four 16-byte pieces per thread (M = 4096, K = 6912: 26.2 us
-// with two, 23.1 with three, 20.8 with four, 24.4 with five), three with the
-// copy of bf16 rows, where four spill.
-constexpr int kNormFwdOneCtaBytes = 16384;
+// Layer norm forward: up to four 16-byte pieces per thread (M = 4096, K = 6912:
+// 26.2 us with two, 23.1 with three, 20.8 with four, 24.4 with five), three with
+// the copy of bf16 rows, where four spill.  A CTA per row while it has at most 256
+// threads, so that an SM holds two (M = 4096, K = 6912 with the copy: 40.8 us as
+// one CTA of 288, 35.6 as two; K = 6144 27.0 as one, 28.6 as two), a cluster
+// beyond, whose CTAs take up to 16 KB of the row each, or 8 KB where bf16 rows
+// leave an 8-bit copy (M = 2048, K = 21504 with the copy 54.7 us against 60.9;
+// without it 34.4 either way).
+constexpr int kNormFwdOneCtaThreads = 256;
 constexpr int kNormFwdPieces = 4;
 constexpr int kNormFwdCopyPieces = 3;
 constexpr int kSmemPerSm = 233472;  // 228 KB
@@ -145,8 +147,8 @@ template <typename T, bool COPY>
 cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
   constexpr int V = Piece<T>::V;
   constexpr int kMost = COPY && sizeof(T) == 2 ? kNormFwdCopyPieces : kNormFwdPieces;
-  constexpr int kOneCta = kNormFwdOneCtaBytes / static_cast<int>(sizeof(T));  // columns
-  constexpr int kSlice = COPY && sizeof(T) == 2 ? kOneCta / 2 : kOneCta;      // of a CTA in a cluster
+  constexpr int kOneCta = kNormFwdOneCtaThreads * kMost * V;  // columns
+  constexpr int kSlice = COPY && sizeof(T) == 2 ? 4096 : kOneCta;  // of a CTA in a cluster
   constexpr int kMaxSplit = (kNormMaxK + kSlice - 1) / kSlice;
   static_assert(kMaxSplit <= 8 && kMaxSplit * ((kSlice / V + 32 * kMost - 1) / (32 * kMost)) <= kNormMaxWarpSums,
                 "a portable cluster takes the longest row, and its warps' sums have a place each");
