@@ -18,7 +18,7 @@
 // lanes, a piece each; its maximum is three or four shuffles.
 //
 // The two kernels are bound by memory for large matrices (M = 2048, K = 21504
-// bf16: copy 0.93 of measured HBM, restore 0.97); a thread has U pieces in
+// bf16: copy 0.95 of measured HBM, restore 0.97); a thread has U pieces in
 // flight at a time, a CTA's width apart.
 #pragma once
 
@@ -78,14 +78,15 @@ BN_DEV void store_act8_pieces(const uint4 (&raw)[N], int64_t at, int stride, con
     Piece<T> x;
     unpack_piece(raw[i], x);
     uint32_t w[V / 4];
-    // scalar steps: a packed product and a packed sum become one fma, which
-    // rounds once where the definition rounds twice (x = amax / 2 then differs)
+    // packed products, but scalar sums: packed ones would become one fma with the
+    // product, which rounds once where the definition rounds twice (x = amax / 2
+    // then differs)
+    const uint64_t k2 = f2(k, k);
 #pragma unroll
     for (int j = 0; j < V / 4; ++j) {
-      w[j] = pack4_s8(f32_to_s8_rne_bits(__fmul_rn(f2_lo(x.p[2 * j]), k)),
-                      f32_to_s8_rne_bits(__fmul_rn(f2_hi(x.p[2 * j]), k)),
-                      f32_to_s8_rne_bits(__fmul_rn(f2_lo(x.p[2 * j + 1]), k)),
-                      f32_to_s8_rne_bits(__fmul_rn(f2_hi(x.p[2 * j + 1]), k)));
+      const uint64_t lo = f2_mul(x.p[2 * j], k2), hi = f2_mul(x.p[2 * j + 1], k2);
+      w[j] = pack4_s8(f32_to_s8_rne_bits(f2_lo(lo)), f32_to_s8_rne_bits(f2_hi(lo)), f32_to_s8_rne_bits(f2_lo(hi)),
+                      f32_to_s8_rne_bits(f2_hi(hi)));
       if (k == 0.0f) w[j] = 0;  // zeros, or a group with an Inf or a NaN
     }
     if (present[i]) {
@@ -95,18 +96,17 @@ BN_DEV void store_act8_pieces(const uint4 (&raw)[N], int64_t at, int stride, con
   }
 }
 
-// Four codes of an 8-bit copy as two pairs of values.  Each code c becomes an
-// fp32 without a conversion instruction: the word with byte c + 128 in its low
-// byte and 0x4B0000 above is 2^23 + 128 + c, and the subtraction is exact.
-BN_DEV void decode_codes4(uint32_t codes, uint64_t scale2, uint64_t* p) {
+// Four codes of an 8-bit copy as two pairs of fp32.  Each code c becomes one
+// without a conversion instruction: the word with byte c + 128 in its low byte
+// and 0x4B0000 above is 2^23 + 128 + c, and the subtraction is exact.
+BN_DEV void codes_to_f32(uint32_t codes, uint64_t* p) {
   const uint32_t w = codes ^ 0x80808080u;
   const uint64_t bias = f2(-8388736.0f, -8388736.0f);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t v = f2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i))),
-                          __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i + 1))));
-    p[i] = f2_mul(f2_add(v, bias), scale2);
-  }
+  for (int i = 0; i < 2; ++i)
+    p[i] = f2_add(f2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i))),
+                     __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | (2 * i + 1)))),
+                  bias);
 }
 
 // The codes of a piece, V bytes.
@@ -116,8 +116,10 @@ BN_DEV uint2 load_codes(const int8_t* p, float) { return make_uint2(__ldg(reinte
 template <typename T>
 BN_DEV void decode_piece(const uint2& codes, float scale, Piece<T>& x) {
   const uint64_t s2 = f2(scale, scale);
-  decode_codes4(codes.x, s2, x.p);
-  if constexpr (Piece<T>::V == 8) decode_codes4(codes.y, s2, x.p + Piece<T>::V / 4);
+  codes_to_f32(codes.x, x.p);
+  if constexpr (Piece<T>::V == 8) codes_to_f32(codes.y, x.p + 2);
+#pragma unroll
+  for (int i = 0; i < Piece<T>::V / 2; ++i) x.p[i] = f2_mul(x.p[i], s2);
 }
 
 constexpr int kAct8Threads = 256;

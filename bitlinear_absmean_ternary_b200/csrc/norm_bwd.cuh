@@ -26,7 +26,9 @@
 // below that by what a grid costs before its first batch and after its last,
 // about 4.5 us (K = 2560 without the sums 14.3 us, 0.68, at M = 4096), and by the
 // join, 3.5 us more.  8-bit copies save bytes but not time here (M = 2048,
-// K = 21504 RMSNorm 52.1 us): their codes take more instructions than bf16.
+// K = 21504 RMSNorm 50.4 us): their codes take more instructions than bf16.  So
+// they enter the products as they are, and their scale goes into the factor:
+// n = code (scale rstd) - mean rstd (52.5 us with scaled values).
 #pragma once
 
 #include "norm.cuh"
@@ -169,24 +171,23 @@ __global__ void __launch_bounds__(kNormMaxThreads)
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) acc_g[j][i] = acc_b[j][i] = 0;
 
-  // dy and x of piece j of a row in the ring; s: its scale
+  // dy and x of piece j of a row in the ring, x in units of its scale; and f in
+  // those units, for a product with x
   const uint32_t my_dy = smem_addr(ring) + 16 * t, my_x = smem_addr(ring) + x_at + XB * t;
-  auto values = [&](int row_at, int j, float s, Piece<T>& d, Piece<T>& x) {
+  auto values = [&](int row_at, int j, Piece<T>& d, Piece<T>& x) {
     unpack_piece(lds128_again(my_dy + row_at + 16 * j * team), d);
     const uint32_t at = my_x + row_at + XB * j * team;
     if constexpr (!COPY) {
       unpack_piece(lds128_again(at), x);
+    } else if constexpr (V == 8) {
+      const uint2 q = lds64_again(at);
+      codes_to_f32(q.x, x.p);
+      codes_to_f32(q.y, x.p + 2);
     } else {
-      const uint64_t s2 = f2(s, s);
-      if constexpr (V == 8) {
-        const uint2 q = lds64_again(at);
-        decode_codes4(q.x, s2, x.p);
-        decode_codes4(q.y, s2, x.p + 2);
-      } else {
-        decode_codes4(lds32_again(at), s2, x.p);
-      }
+      codes_to_f32(lds32_again(at), x.p);
     }
   };
+  auto per_code = [&](uint64_t f, float s) { return COPY ? f2_mul(f, f2(s, s)) : f; };
 
   const float inv_k = 1.0f / static_cast<float>(a.K);
   const int val = lane / kLanes, e0 = lane % kLanes;
@@ -223,20 +224,28 @@ __global__ void __launch_bounds__(kNormMaxThreads)
       for (int r = 0; r < R; ++r) {
         if (r == 0 || row + r < rows) {
           Piece<T> d, x;
-          values(base + r * row_bytes, j, COPY ? scale[COPY ? r : 0][j] : 0.0f, d, x);
+          const float s = COPY ? scale[COPY ? r : 0][j] : 0.0f;
+          values(base + r * row_bytes, j, d, x);
+          const uint64_t xr = per_code(r2[r], s);
+          uint64_t q0 = COPY ? 0 : s0[r], q1 = COPY ? 0 : s1[r];  // RMSNorm: of the codes
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) {
             const uint64_t tt = f2_mul(d.p[i], gain.p[i]);
             if constexpr (RMS) {
-              s0[r] = f2_fma(x.p[i], x.p[i], s0[r]);
-              s1[r] = f2_fma(tt, x.p[i], s1[r]);
+              q0 = f2_fma(x.p[i], x.p[i], q0);
+              q1 = f2_fma(tt, x.p[i], q1);
             } else {
-              const uint64_t nn = f2_fma(x.p[i], r2[r], c2[r]);
+              const uint64_t nn = f2_fma(x.p[i], xr, c2[r]);
               s0[r] = f2_add(s0[r], tt);
               s1[r] = f2_fma(tt, nn, s1[r]);
               acc_g[j][i] = f2_fma(d.p[i], nn, acc_g[j][i]);
               acc_b[j][i] = f2_add(acc_b[j][i], d.p[i]);
             }
+          }
+          if constexpr (RMS) {
+            const uint64_t s2 = f2(s, s);
+            s0[r] = COPY ? f2_fma(f2_mul(q0, s2), s2, s0[r]) : q0;
+            s1[r] = COPY ? f2_fma(q1, s2, s1[r]) : q1;
           }
         }
       }
@@ -309,16 +318,18 @@ __global__ void __launch_bounds__(kNormMaxThreads)
       for (int r = 0; r < R; ++r) {
         if (r == 0 || row + r < rows) {
           Piece<T> d, x, o;
-          values(base + r * row_bytes, j, COPY ? scale[COPY ? r : 0][j] : 0.0f, d, x);
+          const float s = COPY ? scale[COPY ? r : 0][j] : 0.0f;
+          values(base + r * row_bytes, j, d, x);
+          const uint64_t xr = per_code(r2[r], s), xb = per_code(b2[r], s);
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) {
             const uint64_t tt = f2_mul(d.p[i], gain.p[i]);
             if constexpr (RMS) {
-              const uint64_t nn = f2_mul(x.p[i], r2[r]);
+              const uint64_t nn = f2_mul(x.p[i], xr);
               acc_g[j][i] = f2_fma(nn, d.p[i], acc_g[j][i]);
               o.p[i] = f2_fma(tt, r2[r], f2_mul(nn, b2[r]));
             } else {
-              o.p[i] = f2_fma(tt, r2[r], f2_fma(x.p[i], b2[r], a2[r]));
+              o.p[i] = f2_fma(tt, r2[r], f2_fma(x.p[i], xb, a2[r]));
             }
           }
           if (ok[j]) *reinterpret_cast<uint4*>(dx + r * step + j * team * V) = pack_piece(o);
