@@ -14,9 +14,9 @@ using namespace bitnet_host;
 constexpr int64_t kNormMaxK = 32768;
 
 // Backward passes: a CTA per row up to kNormBwdOneCtaK columns (4096 in fp32), a
-// cluster of CTAs of at most kNormBwdSliceK columns beyond (M = 4096, K = 6912
-// RMSNorm 33.2 us as two CTAs, 35.0 as one; M = 2048, K = 5376 layer norm 19.2
-// in one CTA, 19.9 in two).  Up to three 16-byte pieces per thread of bf16
+// cluster of CTAs of at most kNormBwdSliceK columns beyond (layer norm of
+// M = 4096, K = 6912 36.4 us as two CTAs, 39.9 as one; of M = 2048, K = 5376 18.7
+// in one CTA, 19.8 in two).  Up to three 16-byte pieces per thread of bf16
 // (M = 2048, K = 21504: layer norm 56.6 us with two, 53.2 with three; RMSNorm
 // 51.7 with two, 49.2 with three or four), four of fp32.
 constexpr int kNormBwdOneCtaK = 6144;

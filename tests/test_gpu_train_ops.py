@@ -303,9 +303,10 @@ def test_rmsnorm_backward(dev, M, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_norms_at_every_width(dev, dtype):
-    """Every K the norms take, three rows each."""
-    M, zero = 3, torch.zeros(3, dtype=torch.float64, device=dev)
+@pytest.mark.parametrize("M", [3, 37])
+def test_norms_at_every_width(dev, M, dtype):
+    """Every K the norms take, with the column sums of one CTA and with those of several."""
+    zero = torch.zeros(M, dtype=torch.float64, device=dev)
     big_x, big_dy = tensor(dev, M, 32768, dtype, 5, shift=0.3), tensor(dev, M, 32768, dtype, 6, scale=0.01, loud=False)
     big_g, big_b = vector(dev, 32768, dtype, 1), vector(dev, 32768, dtype, 2, -0.3, 0.3)
     for K in range(64, 32768 + 64, 64):
