@@ -192,8 +192,10 @@ __global__ void __launch_bounds__(kNormMaxThreads)
   const float inv_k = 1.0f / static_cast<float>(a.K);
   const int val = lane / kLanes, e0 = lane % kLanes;
   T* dx = static_cast<T*>(a.dx) + first + t * V;
-  int dead = -1;  // the batch at which a wait gave up: no more waits or fills, the results are lost
-  int b = 0;      // the batch; its parity is its stage
+  // The batch at which a wait of this thread gave up: no more waits or fills, no
+  // more arrivals on sent[] or sums sent (end_of_cluster); the results are lost.
+  int dead = -1;
+  int b = 0;  // the batch; its parity is its stage
   for (int row = 0; row < rows; row += R, ++b) {
     const float rstd = rstd_n, shift = -mean_n * rstd_n;
     float scale[COPY ? R : 1][C];
@@ -270,14 +272,16 @@ __global__ void __launch_bounds__(kNormMaxThreads)
         float mine[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) mine[i] = __shfl_sync(0xffffffffu, k, i * kLanes);
-        if (tid == 0) mbar_arrive_expect_tx(&sent[b & 1], static_cast<uint32_t>(entries * NV * 4));
-        if (lane < split) {
-          const uint32_t to = mapa_shared(smem_addr(buf + (rank * tw + warp) * NV), lane);
-          const uint32_t bar = mapa_shared(smem_addr(&sent[b & 1]), lane);
+        if (dead < 0) {
+          if (tid == 0) mbar_arrive_expect_tx(&sent[b & 1], static_cast<uint32_t>(entries * NV * 4));
+          if (lane < split) {
+            const uint32_t to = mapa_shared(smem_addr(buf + (rank * tw + warp) * NV), lane);
+            const uint32_t bar = mapa_shared(smem_addr(&sent[b & 1]), lane);
 #pragma unroll
-          for (int i = 0; i < NV; i += 4) send_cluster(to + 4 * i, mine + i, bar);
+            for (int i = 0; i < NV; i += 4) send_cluster(to + 4 * i, mine + i, bar);
+          }
+          if (!mbar_wait_idle(&sent[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
         }
-        if (dead < 0 && !mbar_wait_idle(&sent[b & 1], static_cast<uint32_t>(b >> 1) & 1u)) dead = b;
       }
       k = 0.0f;
 #pragma unroll 1
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
   // After a timeout: the copies still in flight land before shared memory goes away.
   if (dead >= 0 && t == 0)
     for (int i = dead; i < dead + 2 && i * R < rows; ++i) mbar_wait(&my_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u);
-  if constexpr (MODE == kClusterTeam) cluster_sync();  // nothing more is sent to a CTA that has ended
+  if constexpr (MODE == kClusterTeam) end_of_cluster(sent, dead, tid);
 
   if (a.dgain == nullptr && a.dbias == nullptr) return;
   // The teams' column sums, added in order: teams 1, 2, ... leave theirs in

@@ -156,7 +156,9 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   const float inv_k = 1.0f / static_cast<float>(a.K);
   const uint32_t mine = smem_addr(ring) + 16 * t, pivot_at = smem_addr(ring) + 16 * 32 * warp;
   int64_t at = first + t * V;  // of this thread's first piece in the row at work
-  int dead = -1;               // the batch at which a wait gave up: no more waits or fills, the results are lost
+  // The batch at which a wait of this thread gave up: no more waits or fills, no
+  // more arrivals on sent[] or sums sent (end_of_cluster); the results are lost.
+  int dead = -1;
   int b = 0;
   for (int row = 0; row < rows; row += R, ++b) {
     const int stage = b & 1;
@@ -219,13 +221,15 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
         if ((lane & 7) == 0) reinterpret_cast<float*>(buf + warp)[lane >> 3] = k;
         team_sync(1 + my_team, team);
       } else {
-        if (tid == 0) mbar_arrive_expect_tx(&sent[stage], static_cast<uint32_t>(split * tw * 16));
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, k, 8 * i);
-        if (lane < split)
-          send_cluster(mapa_shared(smem_addr(buf + rank * tw + warp), lane), v, mapa_shared(smem_addr(&sent[stage]), lane));
-        if (dead < 0 && !mbar_wait_idle(&sent[stage], parity)) dead = b;
+        if (dead < 0) {
+          if (tid == 0) mbar_arrive_expect_tx(&sent[stage], static_cast<uint32_t>(split * tw * 16));
+          if (lane < split)
+            send_cluster(mapa_shared(smem_addr(buf + rank * tw + warp), lane), v, mapa_shared(smem_addr(&sent[stage]), lane));
+          if (!mbar_wait_idle(&sent[stage], parity)) dead = b;
+        }
       }
       const float4 e0 = buf[0];
       const float m0 = e0.x * inv_first, m1 = e0.z * inv_first;
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   // After a timeout: the copies still in flight land before shared memory goes away.
   if (dead >= 0 && t == 0)
     for (int i = dead; i < dead + 2 && i * R < rows; ++i) mbar_wait(&my_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u);
-  if constexpr (MODE == kClusterTeam) cluster_sync();  // nothing more is sent to a CTA that has ended
+  if constexpr (MODE == kClusterTeam) end_of_cluster(sent, dead, tid);
   pdl_launch_dependents();
 }
 

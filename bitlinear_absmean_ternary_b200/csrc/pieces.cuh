@@ -148,6 +148,22 @@ BN_DEV void send_cluster(uint32_t cluster_addr, const float* v, uint32_t cluster
       : "memory");
 }
 
+// The end of a CTA that its cluster sends sums to, two phases of sent[] taking
+// turns by batch.  Behind the barrier no peer sends any more.  A thread whose
+// waits all ended well knows that everything has arrived.  One whose wait gave up
+// at batch `dead` has neither arrived on a phase nor sent anything since: the
+// phase it would have used may be open still, and sums sent out of turn overwrite
+// some that are yet to be read.  Without them no peer gets past batch dead + 1, so
+// sums of these two batches can be on their way; their phases may never complete,
+// but the bounded waits leave far more time than sending takes before shared
+// memory goes away.
+BN_DEV void end_of_cluster(uint64_t (&sent)[2], int dead, int tid) {
+  __syncwarp();
+  cluster_sync();
+  if (dead >= 0 && tid == 0)
+    for (int i = dead; i < dead + 2; ++i) mbar_wait_idle(&sent[i & 1], static_cast<uint32_t>(i >> 1) & 1u);
+}
+
 // ------------------------------------------------------------ reductions
 
 // Sums of N (2, 4 or 8) values over the warp: value i ends up in the 32 / N
