@@ -10,18 +10,27 @@
 // 7.5 each, so C is as large as divides the row well (with 16 columns per thread
 // M = 2048, K = 21504 took 41.0 us, with 32 34.4: 0.80 of measured HBM).
 //
-// One stage of sums.  A warp sums x and (x - p)^2, p the mean of its first
-// piece, and makes of them its sum S_w and the squares about its own mean
+// The variance comes from differences throughout, so that a row far from zero
+// keeps its digits.  A warp sums d = x - p and d^2 about a pivot p, which gives its
+// mean and the squares about it:
 //
-//   Q_w = sum (x - p)^2 - (S_w - n_w p)^2 / n_w.
+//   mean_w = p + D_w / n_w,   Q_w = sum d^2 - D_w^2 / n_w
 //
-// The V values behind p alone have squares V (p - mean_w)^2 about mean_w, so the
-// first term is at most 1 + n_w / V times Q_w even with an outlier among them,
-// and about Q_w for others, whatever the row's mean: little cancels.  The team
-// joins the warps' about the first warp's mean c = S_0 / n_0:
+// and the team joins them about the first warp's, delta_w = mean_w - mean_0:
 //
-//   mean = sum S_w / K,  K var = sum (Q_w + n_w (S_w / n_w - c)^2) - K (mean - c)^2
+//   mean = mean_0 + sum n_w delta_w / K
+//   K var = sum (Q_w + n_w delta_w^2) - K (mean - mean_0)^2
 //
+// fp32: p is the warp's mean, summed first, and mean_w travels as the two numbers
+// p and D_w / n_w, as delta_w can be smaller than the rounding of their sum.  At a
+// mean 10^4 times the spread the variance is right to 2e-7 of itself (8e-4 when x
+// was summed itself), and with a row's first columns 1000 times the others to
+// 6e-7 (2e-5 about the first piece).  bf16: p is the mean of the warp's first piece
+// and mean_w one number; values of eight bits hold no spread small enough to need
+// more.  The squares about p are at most 1 + n_w / V times Q_w, even if the piece is
+// all outliers.  The warp's mean as p costs bf16 4 to 8 % (M = 2048, K = 21504
+// 33.9 -> 36.1 us), fp32 2 % (M = 1024, K = 21504 32.4 -> 33.1 us; with the copy
+// 40.8 -> 44.2).
 // In a cluster the warps' sums travel by st.async, as in the backward kernel.
 //
 // Other forms measured at M = 2048, K = 21504 (M = 4096, K = 2560): a CTA per
@@ -61,9 +70,11 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
     layernorm_kernel(const NormFwd a, int team, int split, int cols) {
   constexpr int V = Piece<T>::V, R = 2;
   constexpr int kEntries = MODE == kClusterTeam ? kNormMaxWarpSums : 16;
+  constexpr bool kFar = sizeof(T) == 4;  // the type can hold a row whose mean is many times its spread
+  constexpr int kParts = kFar ? 2 : 1;   // 16-byte parts of a warp's sums
   constexpr int kPerLane = MODE == kClusterTeam ? 2 : 1;  // entries a lane joins
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float4 red[2][kEntries];  // of each warp: S_w and Q_w of both rows
+  __shared__ __align__(16) float4 red[2][kEntries * kParts];  // of each warp: mean_w and Q_w of both rows
   __shared__ __align__(8) uint64_t full[kNormFwdMaxTeams][2];
   __shared__ __align__(8) uint64_t sent[2];
 
@@ -110,13 +121,11 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
     return static_cast<float>(n);
   };
   const float n_mine = columns(rank, warp), inv_mine = n_mine > 0.0f ? 1.0f / n_mine : 0.0f;
-  const float inv_first = 1.0f / columns(0, 0);
-  float n_of[kPerLane], inv_of[kPerLane];  // of entries lane, lane + 32
+  float n_of[kPerLane];  // of entries lane, lane + 32
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 32 * i;
     n_of[i] = e < split * tw ? columns(e / tw, e % tw) : 0.0f;
-    inv_of[i] = n_of[i] > 0.0f ? 1.0f / n_of[i] : 0.0f;
   }
   if constexpr (MODE == kClusterTeam) cluster_sync();
   else __syncthreads();
@@ -155,6 +164,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
 
   const float inv_k = 1.0f / static_cast<float>(a.K);
   const uint32_t mine = smem_addr(ring) + 16 * t, pivot_at = smem_addr(ring) + 16 * 32 * warp;
+  const int lane_row = lane >> 4;  // of the batch: the row whose sums this lane holds
   int64_t at = first + t * V;  // of this thread's first piece in the row at work
   // The batch at which a wait of this thread gave up: no more waits or fills, no
   // more arrivals on sent[] or sums sent (end_of_cluster); the results are lost.
@@ -170,28 +180,48 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
 #pragma unroll
       for (int j = 0; j < C; ++j) raw[r][j] = lds128_again(mine + (stage * R + r) * row_bytes + 16 * j * team);
 
-    // the warp's sums about its pivots: value i of {S, Q of row 0, S, Q of row 1}
-    // ends up in lanes 8 i .. 8 i + 7
-    float sums[4], pivot[R];
+    // the pivots
+    float my_pivot;  // of the lane's row
+    if constexpr (kFar) {
+      float s[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r) {
+        uint64_t s0 = 0;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {  // places past the row's columns are zero
+          Piece<T> x;
+          unpack_piece(raw[r][j], x);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) s0 = f2_add(s0, x.p[i]);
+        }
+        s[r] = f2_lo(s0) + f2_hi(s0);
+      }
+      my_pivot = finite_or_zero(warp_sums(s, lane) * inv_mine);
+    } else {
       Piece<T> x;
-      unpack_piece(lds128_again(pivot_at + (stage * R + r) * row_bytes), x);
+      unpack_piece(lds128_again(pivot_at + (stage * R + lane_row) * row_bytes), x);
       uint64_t s0 = x.p[0];
 #pragma unroll
       for (int i = 1; i < V / 2; ++i) s0 = f2_add(s0, x.p[i]);
-      pivot[r] = (f2_lo(s0) + f2_hi(s0)) * (1.0f / V);
-      const uint64_t p2 = f2(-pivot[r], -pivot[r]);
-      s0 = 0;
-      uint64_t s1 = 0;
+      my_pivot = finite_or_zero((f2_lo(s0) + f2_hi(s0)) * (1.0f / V));
+    }
+    // the warp's sums about its pivots: value i of {D, Q of row 0, D, Q of row 1}
+    // ends up in lanes 8 i .. 8 i + 7
+    float sums[4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float p = __shfl_sync(0xffffffffu, my_pivot, 16 * r);
+      const uint64_t p2 = f2(-p, -p);
+      uint64_t s0 = 0, s1 = 0;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
+        Piece<T> x;
         unpack_piece(raw[r][j], x);
         uint64_t t0 = 0, t1 = 0;
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
           const uint64_t d = f2_add(x.p[i], p2);
-          t0 = f2_add(t0, x.p[i]);
+          t0 = f2_add(t0, d);
           t1 = f2_fma(d, d, t1);
         }
         if (ok[j]) {
@@ -203,55 +233,77 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       sums[2 * r + 1] = f2_lo(s1) + f2_hi(s1);
     }
     float k = warp_sums(sums, lane);
-    const float off = __shfl_xor_sync(0xffffffffu, k, 8) - n_mine * (lane & 16 ? pivot[1] : pivot[0]);
-    if (lane & 8) k -= off * off * inv_mine;
+    const bool of_squares = lane & 8;
+    const float other = __shfl_xor_sync(0xffffffffu, k, 8);
+    k = of_squares ? k - other * other * inv_mine : k * inv_mine;
 
-    float mean[R], var[R];
+    // k: in the lanes of Q the variance, in the lanes of D mean - base
+    float base = my_pivot;
     if constexpr (MODE == kWarpTeam) {
       __syncwarp();
-      k *= inv_k;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        mean[r] = __shfl_sync(0xffffffffu, k, 16 * r);
-        var[r] = __shfl_sync(0xffffffffu, k, 16 * r + 8);
-      }
+      if (of_squares) k *= inv_k;
     } else {
-      float4* buf = &red[stage][my_team * tw];
+      // of each warp {mean_w, Q_w of row 0, the same of row 1}; fp32: mean_w as p + its rest, the rests behind
+      float4* buf = &red[stage][my_team * tw * kParts];
+      const float rest = k;
+      if (!of_squares) k = kFar ? my_pivot : k + my_pivot;
       if constexpr (MODE == kCtaTeam) {
-        if ((lane & 7) == 0) reinterpret_cast<float*>(buf + warp)[lane >> 3] = k;
+        float* to = reinterpret_cast<float*>(buf + warp * kParts) + (lane >> 3);
+        if ((lane & 7) == 0) {
+          to[0] = k;
+          if constexpr (kFar) to[4] = rest;
+        }
         team_sync(1 + my_team, team);
       } else {
-        float v[4];
+        float v[4 * kParts];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, k, 8 * i);
+        for (int i = 0; i < 4; ++i) {
+          v[i] = __shfl_sync(0xffffffffu, k, 8 * i);
+          if constexpr (kFar) v[4 + i] = i & 1 ? 0.0f : __shfl_sync(0xffffffffu, rest, 8 * i);
+        }
         if (dead < 0) {
-          if (tid == 0) mbar_arrive_expect_tx(&sent[stage], static_cast<uint32_t>(split * tw * 16));
-          if (lane < split)
-            send_cluster(mapa_shared(smem_addr(buf + rank * tw + warp), lane), v, mapa_shared(smem_addr(&sent[stage]), lane));
+          if (tid == 0) mbar_arrive_expect_tx(&sent[stage], static_cast<uint32_t>(split * tw * kParts * 16));
+          if (lane < split) {
+            const uint32_t to = mapa_shared(smem_addr(buf + (rank * tw + warp) * kParts), lane);
+            const uint32_t bar = mapa_shared(smem_addr(&sent[stage]), lane);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) send_cluster(to + 16 * i, v + 4 * i, bar);
+          }
           if (!mbar_wait_idle(&sent[stage], parity)) dead = b;
         }
       }
-      const float4 e0 = buf[0];
-      const float m0 = e0.x * inv_first, m1 = e0.z * inv_first;
+      const float4 e0 = buf[0], r0 = buf[kParts - 1];
+      const float m0 = finite_or_zero(e0.x), m1 = finite_or_zero(e0.z);
+      const float rest0 = kFar ? finite_or_zero(r0.x) : 0.0f, rest1 = kFar ? finite_or_zero(r0.z) : 0.0f;
       sums[0] = sums[1] = sums[2] = sums[3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
         if (n_of[i] > 0.0f) {
-          const float4 e = buf[lane + 32 * i];
-          const float d0 = e.x * inv_of[i] - m0, d1 = e.z * inv_of[i] - m1;
-          sums[0] += e.x;
-          sums[1] += e.y + n_of[i] * d0 * d0;
-          sums[2] += e.z;
-          sums[3] += e.w + n_of[i] * d1 * d1;
+          const float4 e = buf[(lane + 32 * i) * kParts];
+          float d0 = e.x - m0, d1 = e.z - m1;
+          if constexpr (kFar) {
+            const float4 r = buf[(lane + 32 * i) * kParts + 1];
+            d0 += r.x - rest0;
+            d1 += r.z - rest1;
+          }
+          const float nd0 = n_of[i] * d0, nd1 = n_of[i] * d1;
+          sums[0] += nd0;
+          sums[1] += e.y + nd0 * d0;
+          sums[2] += nd1;
+          sums[3] += e.w + nd1 * d1;
         }
       }
-      k = warp_sums(sums, lane);
+      k = warp_sums(sums, lane) * inv_k;
+      const float d = __shfl_xor_sync(0xffffffffu, k, 8);
+      k = of_squares ? k - d * d : k + (lane_row ? rest1 : rest0);
+      base = lane_row ? m1 : m0;
+    }
+    k = of_squares ? rsqrtf((k < 0.0f ? 0.0f : k) + a.eps) : base + k;  // NaN stays NaN
+    float mean[R], rstd[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        mean[r] = __shfl_sync(0xffffffffu, k, 16 * r) * inv_k;
-        const float d = mean[r] - (r == 0 ? m0 : m1);
-        var[r] = __shfl_sync(0xffffffffu, k, 16 * r + 8) * inv_k - d * d;
-      }
+    for (int r = 0; r < R; ++r) {
+      mean[r] = __shfl_sync(0xffffffffu, k, 16 * r);
+      rstd[r] = __shfl_sync(0xffffffffu, k, 16 * r + 8);
     }
     // every thread of the team has its values of the stage in registers
     if (t == 0 && row + 2 * R < rows && dead < 0) {
@@ -259,9 +311,6 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       fill(row + 2 * R, stage);
     }
 
-    float rstd[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) rstd[r] = rsqrtf((var[r] < 0.0f ? 0.0f : var[r]) + a.eps);  // NaN stays NaN
     const bool two = row + 1 < rows;
     if (t == 0 && rank == 0) {
 #pragma unroll

@@ -56,6 +56,12 @@ BN_DEV void unpack_piece(const uint4& u, Piece<float>& r) {
   r.p[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
 
+BN_DEV float to_float(float v) { return v; }
+BN_DEV float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// v, or 0 in the place of an Inf or a NaN.
+BN_DEV float finite_or_zero(float v) { return fabsf(v) < __uint_as_float(0x7F800000u) ? v : 0.0f; }
+
 BN_DEV uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
