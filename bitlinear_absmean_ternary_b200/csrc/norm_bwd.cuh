@@ -17,6 +17,12 @@
 // mbarrier of the receiver), so no fence waits for the stores of dx, as the
 // cluster barrier's release would: M = 2048, K = 21504 took 108 us with that.
 //
+// n is (x - mean) rstd, one rounding each, whatever the mean: as x rstd - mean rstd
+// it was off by half a step of mean rstd, in dgain too.  dx of bf16 rows keeps that
+// form, where it costs 2^-24 mean rstd of the term with n, and dx itself is stored
+// to 2^-8 (both uses centred: M = 2048, K = 21504 54.1 -> 56.6 us, the sums alone
+// 54.7; fp32 M = 1024 52.5 -> 54.1 with both).
+//
 // At the end the teams of a CTA add their column sums in order and write one
 // partial row per CTA (cluster), which norm_join_kernel adds in order; one
 // partial row alone is the result.
@@ -55,6 +61,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
   constexpr int V = Piece<T>::V;
   constexpr int NV = 2 * R, kLanes = 32 / NV;  // sums of a batch, lanes that hold each
   constexpr int XB = COPY ? V : 16;            // bytes of x per piece
+  constexpr bool kCentredDx = sizeof(T) == 4;  // n in dx from x - mean
   constexpr int kRed = MODE == kWarpTeam ? 4 : MODE == kCtaTeam ? NV * 16 : NV * kNormMaxWarpSums;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[2][kRed];  // [warp][value], teams one after the other
@@ -187,6 +194,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
       codes_to_f32(lds32_again(at), x.p);
     }
   };
+  auto centred = [&](uint64_t x, float s, uint64_t c) { return COPY ? f2_fma(x, f2(s, s), c) : f2_add(x, c); };
   auto per_code = [&](uint64_t f, float s) { return COPY ? f2_mul(f, f2(s, s)) : f; };
 
   const float inv_k = 1.0f / static_cast<float>(a.K);
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
   int dead = -1;
   int b = 0;  // the batch; its parity is its stage
   for (int row = 0; row < rows; row += R, ++b) {
-    const float rstd = rstd_n, shift = -mean_n * rstd_n;
+    const float rstd = rstd_n, mean = mean_n;
     float scale[COPY ? R : 1][C];
     if constexpr (COPY) {
 #pragma unroll
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
     for (int r = 0; r < R; ++r) {
       s0[r] = s1[r] = 0;
       const float rr = RMS ? 0.0f : __shfl_sync(0xffffffffu, rstd, 2 * kLanes * r);
-      const float cc = RMS ? 0.0f : __shfl_sync(0xffffffffu, shift, 2 * kLanes * r);
+      const float cc = RMS ? 0.0f : -__shfl_sync(0xffffffffu, mean, 2 * kLanes * r);
       r2[r] = f2(rr, rr);
       c2[r] = f2(cc, cc);
     }
@@ -228,7 +236,6 @@ __global__ void __launch_bounds__(kNormMaxThreads)
           Piece<T> d, x;
           const float s = COPY ? scale[COPY ? r : 0][j] : 0.0f;
           values(base + r * row_bytes, j, d, x);
-          const uint64_t xr = per_code(r2[r], s);
           uint64_t q0 = COPY ? 0 : s0[r], q1 = COPY ? 0 : s1[r];  // RMSNorm: of the codes
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) {
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
               q0 = f2_fma(x.p[i], x.p[i], q0);
               q1 = f2_fma(tt, x.p[i], q1);
             } else {
-              const uint64_t nn = f2_fma(x.p[i], xr, c2[r]);
+              const uint64_t nn = f2_mul(centred(x.p[i], s, c2[r]), r2[r]);
               s0[r] = f2_add(s0[r], tt);
               s1[r] = f2_fma(tt, nn, s1[r]);
               acc_g[j][i] = f2_fma(d.p[i], nn, acc_g[j][i]);
@@ -290,9 +297,9 @@ __global__ void __launch_bounds__(kNormMaxThreads)
       for (int d = kLanes / 2; d >= 1; d >>= 1) k += __shfl_xor_sync(0xffffffffu, k, d);
     }
 
-    // Lanes of value 2 r: row r's dx = r t + n B + A = r t + x (r B) + (shift B + A),
-    //   RMSNorm     B = -r (r s1 / K), A = 0 (s1 is of t x, and dx = r t + n B is used)
-    //   layer norm  B = -r s1 / K,     A = -r s0 / K
+    // Lanes of value 2 r: row r's dx = r t + n B + A,
+    //   RMSNorm     B = -r (r s1 / K), A = 0 (s1 is of t x)
+    //   layer norm  B = -r s1 / K,     A = -r s0 / K;  n B = (x - mean) (r B), in bf16 x (r B) - mean r B
     const float k1 = __shfl_xor_sync(0xffffffffu, k, kLanes);
     float row_r, row_a = 0.0f, row_b;
     if constexpr (RMS) {
@@ -300,9 +307,8 @@ __global__ void __launch_bounds__(kNormMaxThreads)
       row_b = -row_r * (row_r * k1 * inv_k);
     } else {
       row_r = rstd;
-      row_b = -rstd * (k1 * inv_k);
-      row_a = shift * row_b - rstd * (k * inv_k);
-      row_b *= rstd;
+      row_b = -rstd * (k1 * inv_k) * rstd;
+      row_a = (kCentredDx ? 0.0f : -mean * row_b) - rstd * (k * inv_k);
     }
     uint64_t a2[R], b2[R];
 #pragma unroll
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
           Piece<T> d, x, o;
           const float s = COPY ? scale[COPY ? r : 0][j] : 0.0f;
           values(base + r * row_bytes, j, d, x);
-          const uint64_t xr = per_code(r2[r], s), xb = per_code(b2[r], s);
+          const uint64_t xr = per_code(r2[r], s);
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) {
             const uint64_t tt = f2_mul(d.p[i], gain.p[i]);
@@ -333,7 +339,9 @@ __global__ void __launch_bounds__(kNormMaxThreads)
               acc_g[j][i] = f2_fma(nn, d.p[i], acc_g[j][i]);
               o.p[i] = f2_fma(tt, r2[r], f2_mul(nn, b2[r]));
             } else {
-              o.p[i] = f2_fma(tt, r2[r], f2_fma(x.p[i], xb, a2[r]));
+              const uint64_t rest = kCentredDx ? f2_fma(centred(x.p[i], s, c2[r]), b2[r], a2[r])
+                                               : f2_fma(x.p[i], per_code(b2[r], s), a2[r]);
+              o.p[i] = f2_fma(tt, r2[r], rest);
             }
           }
           if (ok[j]) *reinterpret_cast<uint4*>(dx + r * step + j * team * V) = pack_piece(o);

@@ -8,7 +8,7 @@ roundings."""
 import pytest
 
 import bitlinear_absmean_ternary_b200 as bl
-from test_gpu_train_ops import EPS, U, close, dev, half_step, tensor, vector  # noqa: F401 (dev is a fixture)
+from test_gpu_train_ops import EPS, U, close, dev, half_step, tensor, values64, vector  # noqa: F401 (dev is a fixture)
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -95,3 +95,51 @@ def test_layernorm_mean_of_rows_with_infinities(dev, M, K):
             assert mean[:2].tolist() == [float("inf"), -float("inf")] and torch.isnan(mean[2:4]).all()
             assert torch.isnan(rstd[:4]).all() and torch.isnan(y[:4]).all()
             assert torch.isfinite(mean[4:]).all() and torch.isfinite(rstd[4:]).all() and torch.isfinite(y[4:]).all()
+
+
+def check_backward(dy, x64, mean, rstd, gain, dx, dgain, dbias):
+    """x - mean is one rounding and its product with rstd another, whatever the mean.  dx of bf16 rows takes mean rstd
+    apart: n m2 to a few u |mean| rstd |m2|, far below dx's own half step."""
+    M = dy.shape[0]
+    d, g = dy.double(), gain.double()
+    c, r = mean.double()[:, None], rstd.double()[:, None]
+    n = (x64 - c) * r
+    dn = 2.01 * U * n.abs()
+    t = d * g
+    m1, m2 = t.mean(1, keepdim=True), (t * n).mean(1, keepdim=True)
+    d_m1 = DEPTH * U * t.abs().mean(1, keepdim=True)
+    d_m2 = DEPTH * U * (t * n).abs().mean(1, keepdim=True) + (t.abs() * dn).mean(1, keepdim=True)
+    parts = t.abs() + m1.abs() + (n * m2).abs()
+    want, tol = r * (t - m1 - n * m2), r * (8 * U * parts + d_m1 + n.abs() * d_m2 + dn * m2.abs())
+    if dy.dtype == torch.bfloat16:
+        tol = tol + r * 4 * U * (x64.abs() + c.abs()) * r * m2.abs()
+        tol = tol + half_step(dy.dtype) * (want.abs() + tol)
+    close(dx, want, 1.01 * tol + 1e-38, "dx")
+    close(dgain, (d * n).sum(0), 1.01 * ((M + 8) * U * (d * n).abs() + d.abs() * dn).sum(0) + 1e-38, "dgain")
+    close(dbias, d.sum(0), (M + 8) * U * d.abs().sum(0) + 1e-38, "dbias")
+
+
+@pytest.mark.parametrize("offset", [0.0, 1e3, -1e4, 1e5])
+@pytest.mark.parametrize("M,K", SHAPES)
+def test_layernorm_backward_of_rows_far_from_zero(dev, M, K, offset):
+    x = tensor(dev, M, K, "f32", K, shift=offset, loud=False)
+    # a gradient along n, so that its share of dx counts
+    dy = 0.1 * tensor(dev, M, K, "f32", K + 1, loud=False) + (x - offset)
+    gain = vector(dev, K, "f32", 1)
+    _, mean, rstd, x8, xs = bl.bitnet_layernorm(x, gain, None, EPS, checkpoint=True)
+    check_backward(dy, x.double(), mean, rstd, gain, *bl.bitnet_layernorm_backward(dy, mean, rstd, x=x, gain=gain))
+    check_backward(dy, values64(x8, xs), mean, rstd, gain,
+                       *bl.bitnet_layernorm_backward(dy, mean, rstd, x8=x8, x_scale=xs, gain=gain))
+
+
+@pytest.mark.parametrize("M,K", SHAPES)
+def test_layernorm_backward_of_nearly_constant_bf16_rows(dev, M, K):
+    """Rows of 1000 with one value a step above: a mean of thousands of spreads; and rows of 1000 alone, where n is 0."""
+    x = torch.full((M, K), 1000.0, dtype=torch.bfloat16, device=dev)
+    x[::2, K // 2] = 1008.0
+    dy = tensor(dev, M, K, "bf16", K, scale=0.1, loud=False)
+    gain = vector(dev, K, "bf16", 1)
+    _, mean, rstd, x8, xs = bl.bitnet_layernorm(x, gain, None, EPS, checkpoint=True)
+    check_backward(dy, x.double(), mean, rstd, gain, *bl.bitnet_layernorm_backward(dy, mean, rstd, x=x, gain=gain))
+    check_backward(dy, values64(x8, xs), mean, rstd, gain,
+                   *bl.bitnet_layernorm_backward(dy, mean, rstd, x8=x8, x_scale=xs, gain=gain))
