@@ -20,6 +20,16 @@
 
 namespace bitnet {
 
+// 1 / sqrt(v), off by little more than half a step: CUDA's approximation y, then
+// y (1 + e / 2) with e = 1 - v y^2 taken from v y in two parts.  rsqrtf alone can be
+// two steps off; RN(1 / RN(sqrt(v))) is off by up to one and costs RMSNorm's gradient
+// 1 to 10 % (M = 4096, K = 6912 35.6 -> 39.0 us, so 35.7).
+BN_DEV float rounded_rsqrt(float v) {
+  const float y = rsqrtf(v), h = __fmul_rn(v, y), l = __fmaf_rn(v, y, -h);
+  const float e = __fmaf_rn(-l, y, __fmaf_rn(-h, y, 1.0f));
+  return fabsf(e) < 1.0f ? __fmaf_rn(0.5f * y, e, y) : y;  // y is 0 for an Inf
+}
+
 // Who owns a row: a warp, part or all of a CTA, or a cluster of CTAs.
 enum NormTeam { kWarpTeam, kCtaTeam, kClusterTeam };
 

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
   constexpr int V = Piece<T>::V;
   constexpr int NV = 2 * R, kLanes = 32 / NV;  // sums of a batch, lanes that hold each
   constexpr int XB = COPY ? V : 16;            // bytes of x per piece
-  constexpr bool kCentredDx = sizeof(T) == 4;  // n in dx from x - mean
+  constexpr bool kFine = sizeof(T) == 4;       // dx in fp32: its n from x - mean, and from restored values
   constexpr int kRed = MODE == kWarpTeam ? 4 : MODE == kCtaTeam ? NV * 16 : NV * kNormMaxWarpSums;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[2][kRed];  // [warp][value], teams one after the other
@@ -303,12 +303,12 @@ __global__ void __launch_bounds__(kNormMaxThreads)
     const float k1 = __shfl_xor_sync(0xffffffffu, k, kLanes);
     float row_r, row_a = 0.0f, row_b;
     if constexpr (RMS) {
-      row_r = rsqrtf(k * inv_k + a.eps);
+      row_r = rounded_rsqrt(k * inv_k + a.eps);
       row_b = -row_r * (row_r * k1 * inv_k);
     } else {
       row_r = rstd;
       row_b = -rstd * (k1 * inv_k) * rstd;
-      row_a = (kCentredDx ? 0.0f : -mean * row_b) - rstd * (k * inv_k);
+      row_a = (kFine ? 0.0f : -mean * row_b) - rstd * (k * inv_k);
     }
     uint64_t a2[R], b2[R];
 #pragma unroll
@@ -335,11 +335,11 @@ __global__ void __launch_bounds__(kNormMaxThreads)
           for (int i = 0; i < V / 2; ++i) {
             const uint64_t tt = f2_mul(d.p[i], gain.p[i]);
             if constexpr (RMS) {
-              const uint64_t nn = f2_mul(x.p[i], xr);
+              const uint64_t nn = kFine && COPY ? f2_mul(f2_mul(x.p[i], f2(s, s)), r2[r]) : f2_mul(x.p[i], xr);
               acc_g[j][i] = f2_fma(nn, d.p[i], acc_g[j][i]);
               o.p[i] = f2_fma(tt, r2[r], f2_mul(nn, b2[r]));
             } else {
-              const uint64_t rest = kCentredDx ? f2_fma(centred(x.p[i], s, c2[r]), b2[r], a2[r])
+              const uint64_t rest = kFine ? f2_fma(centred(x.p[i], s, c2[r]), b2[r], a2[r])
                                                : f2_fma(x.p[i], per_code(b2[r], s), a2[r]);
               o.p[i] = f2_fma(tt, r2[r], rest);
             }

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       k = of_squares ? k - d * d : k + (lane_row ? rest1 : rest0);
       base = lane_row ? m1 : m0;
     }
-    k = of_squares ? rsqrtf((k < 0.0f ? 0.0f : k) + a.eps) : base + k;  // NaN stays NaN
+    k = of_squares ? rounded_rsqrt((k < 0.0f ? 0.0f : k) + a.eps) : base + k;  // NaN stays NaN
     float mean[R], rstd[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {

@@ -1,5 +1,5 @@
-"""GPU tests of the norms' accuracy: rows far from zero, outliers and
-infinities, against 64-bit forms.
+"""GPU tests of the norms' accuracy: rows far from zero, outliers, infinities,
+and the rounding of 1 / sqrt, against 64-bit forms.
 
 Tolerances count fp32's half steps u = 2^-24.  The additions between a value and
 its row's result number at most DEPTH: 16 in a thread (two halves of at most 16
@@ -143,3 +143,60 @@ def test_layernorm_backward_of_nearly_constant_bf16_rows(dev, M, K):
     check_backward(dy, x.double(), mean, rstd, gain, *bl.bitnet_layernorm_backward(dy, mean, rstd, x=x, gain=gain))
     check_backward(dy, values64(x8, xs), mean, rstd, gain,
                    *bl.bitnet_layernorm_backward(dy, mean, rstd, x8=x8, x_scale=xs, gain=gain))
+
+
+def short_values(dev, n, seed):
+    """Values of eight mantissa bits, whose squares add up without a rounding."""
+    gen = torch.Generator().manual_seed(seed)
+    v = torch.rand(n, generator=gen, dtype=torch.float64) * 4 + 0.01
+    return v.to(torch.bfloat16).float().to(dev)
+
+
+def check_r(r, square, eps):
+    """r against 1 / sqrt(RN(square + eps)): half a step, and a second-order rest below a thousandth of one."""
+    want = (square + torch.full_like(square, eps)).double().rsqrt()
+    step = 2.0 ** (torch.floor(torch.log2(want)) - 23)
+    over = (r.double() - want).abs() / step
+    assert float(over.max()) <= 0.501, float(over.max())
+
+
+@pytest.mark.parametrize("K", [64, 256, 2048, 8192, 32768])
+def test_rmsnorm_backward_rounds_r_once(dev, K):
+    """Rows of equal magnitude and a gradient that adds up to nothing along them: dx is r.  K is a power of two, so
+    that the mean square has no rounding."""
+    M = 2048 if K < 20000 else 512
+    v = short_values(dev, M, K)
+    x = v[:, None].repeat(1, K)
+    dy = torch.ones(M, K, device=dev)
+    dy[:, 1::2] = -1.0
+    dx, _ = bl.bitnet_rmsnorm_backward(dy, x=x, rms_eps=EPS)
+    check_r(dx[:, 0], v * v, EPS)
+    assert torch.equal(dx, dx[:, :1] * dy)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [64, 256, 2048, 8192, 32768])
+def test_layernorm_rounds_rstd_once(dev, K, dtype):
+    """Rows of v, -v, v, -v, ...: mean 0, variance v^2, both without a rounding as K is a power of two."""
+    M = 2048 if K < 20000 else 512
+    v = short_values(dev, M, K)
+    x = v[:, None].repeat(1, K)
+    x[:, 1::2] *= -1.0
+    _, mean, rstd = bl.bitnet_layernorm(x.to(torch.bfloat16 if dtype == "bf16" else torch.float32), eps=EPS)
+    assert not mean.any()
+    check_r(rstd, v * v, EPS)
+
+
+def test_norms_of_tiny_and_huge_variance(dev):
+    """eps alone, of any size, and variances that fp32 does not hold: rstd is 1 / sqrt(eps), or 0."""
+    for eps in (1e-38, 1e-30, 1e-12, 1.0, 1e30):
+        x = torch.zeros(3, 128, device=dev)
+        x[1] = 1e25
+        x[1, ::2] = -1e25
+        y, _, rstd = bl.bitnet_layernorm(x, eps=eps)
+        want = torch.tensor(eps, dtype=torch.float32).double() ** -0.5
+        assert abs(float(rstd[0]) - float(want)) <= float(want) * 1.01 * U
+        assert float(rstd[1]) == 0.0 and not y.any()
+        dx, _ = bl.bitnet_rmsnorm_backward(torch.ones_like(x), x=x, rms_eps=eps)
+        assert abs(float(dx[0, 0]) - float(want)) <= float(want) * 1.01 * U
+        assert not dx[1].any()
