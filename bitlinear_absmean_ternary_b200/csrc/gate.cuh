@@ -18,13 +18,14 @@ namespace bitnet {
 
 constexpr int kGateThreads = 256;
 
-template <typename T>
+// r of a piece.  A NaN closes the gate, but one that a copy restores to stands for
+// a whole group that held an Inf or a NaN: it stays (KEEP_NAN), as zeros in its
+// place would pass for the gradients of closed gates.
+template <bool KEEP_NAN, typename T>
 BN_DEV void relu_piece(const Piece<T>& g, Piece<T>& r) {
+  auto relu = [](float v) { return (KEEP_NAN ? !(v <= 0.0f) : v > 0.0f) ? v : 0.0f; };
 #pragma unroll
-  for (int i = 0; i < Piece<T>::V / 2; ++i) {
-    const float lo = f2_lo(g.p[i]), hi = f2_hi(g.p[i]);
-    r.p[i] = f2(lo > 0.0f ? lo : 0.0f, hi > 0.0f ? hi : 0.0f);
-  }
+  for (int i = 0; i < Piece<T>::V / 2; ++i) r.p[i] = f2(relu(f2_lo(g.p[i])), relu(f2_hi(g.p[i])));
 }
 
 template <typename T, bool COPY, int U>
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(kGateThreads)
     Piece<T> fu, fg, r, o;
     unpack_piece(ru[i], fu);
     unpack_piece(rg[i], fg);
-    relu_piece(fg, r);
+    relu_piece<false>(fg, r);
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) o.p[j] = f2_mul(f2_mul(r.p[j], r.p[j]), fu.p[j]);
     if (present[i]) *reinterpret_cast<uint4*>(h + (first + i * kGateThreads) * V) = pack_piece(o);
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kGateThreads)
       unpack_piece(ldg_once(u + p * V), fu);
       unpack_piece(ldg_once(g + p * V), fg);
     }
-    relu_piece(fg, r);
+    relu_piece<COPY>(fg, r);
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) {
       a.p[j] = f2_mul(d.p[j], f2_mul(r.p[j], r.p[j]));

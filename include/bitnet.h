@@ -586,7 +586,8 @@ bitnet_status bitnet_rmsnorm_backward(const void* dy, int dtype, int64_t M, int6
  * bitnet_relu2_gate writes the 8-bit copies of u and g in the same pass when
  * u8, u_scale, g8 and g_scale are given (all four or none).
  * bitnet_relu2_gate_backward reads u and g, or the copies (all of one form,
- * none of the other).
+ * none of the other).  A NaN in g closes the gate; a group of g's copy that holds
+ * an Inf or a NaN gives NaN in all of its du and dg.
  */
 bitnet_status bitnet_relu2_gate(const void* u, const void* g, int dtype, int64_t M, int64_t F, void* h, int8_t* u8,
                                 float* u_scale, int8_t* g8, float* g_scale, void* stream);
