@@ -24,12 +24,14 @@ constexpr int kNormBwdSliceK = 4096;
 constexpr int kNormBwdPieces = 3;
 // Layer norm forward: up to four 16-byte pieces per thread (M = 4096, K = 6912:
 // 26.2 us with two, 23.1 with three, 20.8 with four, 24.4 with five), three with
-// the copy of bf16 rows, where four spill.  A CTA per row while it has at most 256
-// threads, so that an SM holds two (M = 4096, K = 6912 with the copy: 40.8 us as
-// one CTA of 288, 35.6 as two; K = 6144 27.0 as one, 28.6 as two), a cluster
-// beyond, whose CTAs take up to 16 KB of the row each, or 8 KB where bf16 rows
-// leave an 8-bit copy (M = 2048, K = 21504 with the copy 54.7 us against 60.9;
-// without it 34.4 either way).
+// the copy of bf16 rows, where four spill.  A CTA per row while 256 threads of that
+// many pieces hold it, and never more threads than that, so that an SM holds two
+// (M = 4096, K = 6912 with the copy: 40.8 us as one CTA of 288, 35.6 as two;
+// K = 6144 27.0 as one, 28.6 as two; K = 5632 31.1 with 352 threads of two pieces,
+// 26.0 with 256 of three; without the copy K = 2752 18.7 with 352 of one, 12.2 with
+// 192 of two), a cluster beyond, whose CTAs take up to 16 KB of the row each, or
+// 8 KB where bf16 rows leave an 8-bit copy (M = 2048, K = 21504 with the copy
+// 54.7 us against 60.9; without it 34.4 either way).
 constexpr int kNormFwdOneCtaThreads = 256;
 constexpr int kNormFwdPieces = 4;
 constexpr int kNormFwdCopyPieces = 3;
@@ -59,7 +61,7 @@ int64_t norm_most_parts(int64_t M) { return std::min<int64_t>(M, sm_count()); }
 // 16-byte pieces per thread, least to most: the most that leave at most a
 // twelfth of the team's places empty, as empty places cost like full ones; no
 // fewer than keep the team within 512 threads.
-int pieces_per_thread(int pieces, int least, int most) {
+constexpr int pieces_per_thread(int pieces, int least, int most) {
   least = std::max(least, (pieces + kNormMaxThreads - 1) / kNormMaxThreads);
   for (int c = most; c > least; --c) {
     const int places = (pieces + 32 * c - 1) / (32 * c) * 32 * c;
@@ -67,6 +69,23 @@ int pieces_per_thread(int pieces, int least, int most) {
   }
   return least;
 }
+
+// Threads of a layer norm team and their pieces, for `pieces` pieces of a row in a
+// CTA: a CTA of a cluster takes the most pieces, one of its own row no fewer than
+// keep it within kNormFwdOneCtaThreads.
+constexpr int norm_fwd_pieces(int pieces, bool cluster, int most) {
+  return cluster ? most
+                 : pieces_per_thread(pieces, (pieces + kNormFwdOneCtaThreads - 1) / kNormFwdOneCtaThreads, most);
+}
+constexpr int norm_fwd_team(int pieces, int c) { return (pieces + 32 * c - 1) / (32 * c) * 32; }
+
+constexpr bool norm_fwd_teams_fit(int most) {
+  for (int pieces = 1; pieces <= kNormFwdOneCtaThreads * most; ++pieces)
+    if (norm_fwd_team(pieces, norm_fwd_pieces(pieces, false, most)) > kNormFwdOneCtaThreads) return false;
+  return true;
+}
+static_assert(norm_fwd_teams_fit(kNormFwdPieces) && norm_fwd_teams_fit(kNormFwdCopyPieces),
+              "an SM holds two CTAs of every width that has a CTA per row");
 
 // Clusters of this launch that run at the same time: GPCs hold a whole number
 // of them, so it can be less than the SMs would suggest, and a grid of more runs
@@ -155,8 +174,8 @@ cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
   const int split = a.K <= kOneCta ? 1 : (a.K + kSlice - 1) / kSlice;
   const int cols = ((a.K / 64 + split - 1) / split) * 64;
   const int pieces = cols / V;
-  const int c = split > 1 ? kMost : pieces_per_thread(pieces, 1, kMost);
-  const int team = (pieces + 32 * c - 1) / (32 * c) * 32;
+  const int c = norm_fwd_pieces(pieces, split > 1, kMost);
+  const int team = norm_fwd_team(pieces, c);
   const int mode = split > 1 ? kClusterTeam : team > 32 ? kCtaTeam : kWarpTeam;
 #define BN_LN(C)                                                                                     \
   if constexpr (C <= kMost) {                                                                        \
