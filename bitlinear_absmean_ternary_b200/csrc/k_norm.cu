@@ -181,7 +181,8 @@ cudaError_t launch_layernorm(const NormFwd& a, cudaStream_t s) {
   if constexpr (C <= kMost) {                                                                        \
     if (c == C && mode == kWarpTeam) return launch_layernorm_t<T, COPY, kWarpTeam, C>(a, 1, cols, team, s); \
     if (c == C && mode == kCtaTeam) return launch_layernorm_t<T, COPY, kCtaTeam, C>(a, 1, cols, team, s);   \
-    if (c == C) return launch_layernorm_t<T, COPY, kClusterTeam, C>(a, (a.K + cols - 1) / cols, cols, team, s); \
+    if constexpr (C == kMost)                                                                        \
+      if (c == C) return launch_layernorm_t<T, COPY, kClusterTeam, C>(a, (a.K + cols - 1) / cols, cols, team, s); \
   }
   BN_LN(1) BN_LN(2) BN_LN(3) BN_LN(4)
 #undef BN_LN
