@@ -13,18 +13,22 @@ using namespace bitnet_host;
 
 constexpr int64_t kNormMaxK = 32768;
 
-// Backward passes: a CTA per row up to kNormBwdOneCtaK columns (4096 in fp32), a
-// cluster of CTAs of at most kNormBwdSliceK columns beyond (layer norm of
-// M = 4096, K = 6912 36.4 us as two CTAs, 39.9 as one; of M = 2048, K = 5376 18.7
-// in one CTA, 19.8 in two).  Up to three 16-byte pieces per thread of bf16
-// (M = 2048, K = 21504: layer norm 56.6 us with two, 53.2 with three; RMSNorm
-// 51.7 with two, 49.2 with three or four), four of fp32.
+// Backward passes: a CTA per row up to kNormBwdOneCtaK columns, a cluster of CTAs
+// of at most kNormBwdSliceK columns beyond (layer norm of M = 4096, K = 6912 36.4 us
+// as two CTAs, 39.9 as one; of M = 2048, K = 5376 18.7 in one CTA, 19.8 in two; in
+// fp32 26.3 in one, 27.8 in two, and K = 6144 29.6 and 30.6).  Up to three 16-byte
+// pieces per thread of bf16 (M = 2048, K = 21504: layer norm 56.6 us with two, 53.2
+// with three; RMSNorm 51.7 with two, 49.2 with three or four).  Four of fp32: at
+// K = 3840 20.1 us against 20.1 with three (RMSNorm 19.7 and 20.3, from the copy
+// 18.1 and 18.6), at K = 2560 24.9 and 24.6 (25.0 and 25.2, 21.3 and 20.9); in a
+// cluster fewer would make more warps than have a place for their sums.
 constexpr int kNormBwdOneCtaK = 6144;
 constexpr int kNormBwdSliceK = 4096;
 constexpr int kNormBwdPieces = 3;
 // Layer norm forward: up to four 16-byte pieces per thread (M = 4096, K = 6912:
-// 26.2 us with two, 23.1 with three, 20.8 with four, 24.4 with five), three with
-// the copy of bf16 rows, where four spill.  A CTA per row while 256 threads of that
+// 26.2 us with two, 23.1 with three, 20.8 with four, 24.4 with five; fp32 M = 1024,
+// K = 21504 37.4 with three, 33.6 with four, with the copy 47.7 and 44.7), three
+// with the copy of bf16 rows, where four spill.  A CTA per row while 256 threads of that
 // many pieces hold it, and never more threads than that, so that an SM holds two
 // (M = 4096, K = 6912 with the copy: 40.8 us as one CTA of 288, 35.6 as two;
 // K = 6144 27.0 as one, 28.6 as two; K = 5632 31.1 with 352 threads of two pieces,
@@ -221,11 +225,10 @@ cudaError_t launch_norm_backward_t(const NormBwd& a, cudaStream_t s) {
   constexpr int V = Piece<T>::V;
   constexpr int kMost = sizeof(T) == 4 ? 4 : kNormBwdPieces;
   constexpr int kLeast = sizeof(T) == 4 ? 4 : 2;  // in a cluster
-  constexpr int kOneCta = sizeof(T) == 4 ? kNormBwdSliceK : kNormBwdOneCtaK;
   constexpr int kMaxSplit = (kNormMaxK + kNormBwdSliceK - 1) / kNormBwdSliceK;
   static_assert(kMaxSplit <= 8 && kMaxSplit * (kNormBwdSliceK / V / (32 * kLeast)) <= kNormMaxWarpSums,
                 "a portable cluster takes the longest row, and its warps' sums have a place each");
-  const int split = a.K <= kOneCta ? 1 : (a.K + kNormBwdSliceK - 1) / kNormBwdSliceK;
+  const int split = a.K <= kNormBwdOneCtaK ? 1 : (a.K + kNormBwdSliceK - 1) / kNormBwdSliceK;
   const int cols = (a.K / 64 + split - 1) / split * 64;
   const int pieces = cols / V;
   int c = pieces_per_thread(pieces, split > 1 ? kLeast : 1, kMost);
