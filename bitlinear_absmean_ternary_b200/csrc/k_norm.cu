@@ -133,7 +133,8 @@ cudaError_t launch_teams(void (*kern)(KArgs...), int split, int threads, int sme
   if constexpr (MODE == kClusterTeam) {
     // Only the cluster size: clusters placed around a grid that has not ended
     // leave some for a second wave (gate, then layer norm of M = 2048, K = 21504
-    // 94.8 us with programmatic launch, 78.9 without; layer norm alone 39.5, 40.9).
+    // 94.8 us with programmatic launch, 78.9 without; one layer norm with nothing
+    // around it 39.5, 40.9).
     if (clusters > sm_count() / 2 / split) clusters = std::min(clusters, active_clusters(kern, cfg, split, cache));
   } else {
     const int by_regs = 65536 / ((registers + 7) / 8 * 8 * threads);

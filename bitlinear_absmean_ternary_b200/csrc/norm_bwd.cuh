@@ -27,14 +27,15 @@
 // partial row per CTA (cluster), which norm_join_kernel adds in order; one
 // partial row alone is the result.
 //
-// Bound by memory for many rows (K = 2560 without the column sums: 49.1 us, 0.92
-// of measured HBM, at M = 18944; RMSNorm at M = 2048, K = 21504 48.9 us, 0.84),
+// Bound by memory for many rows (K = 2560 without the column sums: 49.3 us, 0.92
+// of measured HBM, at M = 18944; RMSNorm at M = 2048, K = 21504 49.0 us, 0.84),
 // below that by what a grid costs before its first batch and after its last,
-// about 4.5 us (K = 2560 without the sums 14.3 us, 0.68, at M = 4096), and by the
+// about 4.5 us (K = 2560 without the sums 14.5 us, 0.67, at M = 4096), and by the
 // join, 3 us more.  8-bit copies save bytes but not time here (M = 2048,
-// K = 21504 RMSNorm 50.4 us): their codes take more instructions than bf16.  So
-// they enter the products as they are, and their scale goes into the factor:
-// n = code (scale rstd) - mean rstd (52.5 us with scaled values).
+// K = 21504 RMSNorm 50.8 us): their codes take more instructions than bf16.  So
+// they enter the products as they are, and their scale goes into the factor,
+// n = code (scale r) for RMSNorm (52.5 us with scaled values); layer norm's
+// x - mean is one fma of a code.  dx of fp32 rows is made from restored values.
 #pragma once
 
 #include "norm.cuh"

@@ -8,7 +8,7 @@
 // once; its columns' gain and bias stay in shared memory for all rows.  A batch
 // costs a warp about 270 instructions whatever its lanes hold, the values about
 // 7.5 each, so C is as large as divides the row well (with 16 columns per thread
-// M = 2048, K = 21504 took 41.0 us, with 32 34.4: 0.80 of measured HBM).
+// M = 2048, K = 21504 took 41.0 us, with 32 33.9: 0.81 of measured HBM).
 //
 // The variance comes from differences throughout, so that a row far from zero
 // keeps its digits.  A warp sums d = x - p and d^2 about a pivot p, which gives its
@@ -31,14 +31,16 @@
 // all outliers.  The warp's mean as p costs bf16 4 to 8 % (M = 2048, K = 21504
 // 33.9 -> 36.1 us), fp32 2 % (M = 1024, K = 21504 32.4 -> 33.1 us; with the copy
 // 40.8 -> 44.2).
+//
 // In a cluster the warps' sums travel by st.async, as in the backward kernel.
 //
 // Other forms measured at M = 2048, K = 21504 (M = 4096, K = 2560): a CTA per
 // row that reads it three times from L1 or L2 41 us (16.2); a row in the
 // registers of up to 896 threads 60 (19), or of few threads with 80 columns each
 // 77 (14.4); the sums of a batch exchanged while the batch before is finished
-// 43.7 (12.7); this one 34.4 (10.7).  Short calls (M = 4, K = 256: 1.7 us) are a
-// launch and a trip to memory.
+// 43.7 (12.7); this one 33.9 (10.9).  Short calls (M = 4, K = 256 fp32: 1.9 us) are
+// a launch and a trip to memory.  The copy doubles the instructions (M = 2048,
+// K = 21504 34.5 million, 17.1 without) and takes 0.60 of the issue slots: 53.4 us.
 #pragma once
 
 #include "norm.cuh"
