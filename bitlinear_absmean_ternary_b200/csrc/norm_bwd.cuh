@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kNormMaxThreads)
               o.p[i] = f2_fma(tt, r2[r], f2_mul(nn, b2[r]));
             } else {
               const uint64_t rest = kFine ? f2_fma(centred(x.p[i], s, c2[r]), b2[r], a2[r])
-                                               : f2_fma(x.p[i], per_code(b2[r], s), a2[r]);
+                                          : f2_fma(x.p[i], per_code(b2[r], s), a2[r]);
               o.p[i] = f2_fma(tt, r2[r], rest);
             }
           }

@@ -22,15 +22,14 @@
 //   K var = sum (Q_w + n_w delta_w^2) - K (mean - mean_0)^2
 //
 // fp32: p is the warp's mean, summed first, and mean_w travels as the two numbers
-// p and D_w / n_w, as delta_w can be smaller than the rounding of their sum.  At a
-// mean 10^4 times the spread the variance is right to 2e-7 of itself (8e-4 when x
-// was summed itself), and with a row's first columns 1000 times the others to
-// 6e-7 (2e-5 about the first piece).  bf16: p is the mean of the warp's first piece
-// and mean_w one number; values of eight bits hold no spread small enough to need
-// more.  The squares about p are at most 1 + n_w / V times Q_w, even if the piece is
-// all outliers.  The warp's mean as p costs bf16 4 to 8 % (M = 2048, K = 21504
-// 33.9 -> 36.1 us), fp32 2 % (M = 1024, K = 21504 32.4 -> 33.1 us; with the copy
-// 40.8 -> 44.2).
+// p and D_w / n_w, as delta_w can be smaller than the rounding of their sum.  The
+// variance is right to 3e-7 of itself at means of up to 10^5 times the spread (8e-4
+// at 10^4 when x was summed itself), to 3e-6 where up to 100 first columns are 1000
+// times the others.  bf16: p is the mean of the warp's first piece and mean_w one
+// number; 3e-7 at a mean of 50 spreads, 3e-5 where the first piece is 1000 times the
+// others, as the squares about p are at most 1 + n_w / V times Q_w.  The warp's mean
+// as p costs bf16 4 to 8 % (M = 2048, K = 21504 33.9 -> 36.1 us), fp32 2 % (M = 1024,
+// K = 21504 32.4 -> 33.1 us; with the copy 40.8 -> 44.2).
 //
 // In a cluster the warps' sums travel by st.async, as in the backward kernel.
 //
